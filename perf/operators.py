@@ -330,8 +330,8 @@ def _prep_targets(c, g):
                                          torch.full_like(r, -1))
     if c["out"]:
         s["out"] = torch.empty((n, V), dtype=torch.float32, device=DEV)
-    # the library's scratch, which a user's program keeps: 8 bytes a row and slice
-    s["ws"] = torch.empty(8 * n * ((V + 2047) // 2048), dtype=torch.uint8, device=DEV)
+    # scratch that a user's program keeps: 8 bytes a row and 1024 tokens
+    s["ws"] = torch.empty(8 * n * (V // 1024 + 2), dtype=torch.uint8, device=DEV)
     return s
 
 
