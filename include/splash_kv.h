@@ -86,9 +86,14 @@ enum {
                                          up (after 1 s by default, see
                                          splash_set_wait_limit_ns); outputs of that
                                          call undefined */
-  SPLASH_DEVICE_INTERNAL = 4          /* the tensor-core kernel found its shared memory
+  SPLASH_DEVICE_INTERNAL = 4,         /* the tensor-core kernel found its shared memory
                                          misaligned and did nothing */
+  SPLASH_DEVICE_OUT_OF_PAGES = 5      /* the free list cannot serve every sequence
+                                         (splash_build_tables) */
 };
+
+/* Element types of the entry points that take a dtype argument. */
+enum { SPLASH_F32 = 0, SPLASH_BF16 = 1, SPLASH_F16 = 2 };
 
 /* Human-readable name of a SPLASH_* status (static string, never NULL). */
 const char* splash_status_string(int status);
@@ -392,6 +397,190 @@ int splash_verify_attention_fixed_scratch(const uint16_t* q, int num_q_tokens,
                                           int max_block_len, float sm_scale, uint16_t* out,
                                           float* lse, int* device_status,
                                           struct CUstream_st* stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of a verify step. Page tables and slot maps, the projections'
+ * norm, rotation and append, and the target's choices, so that a step's
+ * lengths, pages and tokens stay on the device:
+ *   splash_build_tables -> splash_qkv_append -> splash_verify_attention
+ *   -> (the model's output head) -> splash_choose_targets
+ *   -> splash_accept_commit -> splash_token_state_add
+ * These are this library's own: the Splash pages describe none of them. All
+ * are enqueued on `stream`, allocate nothing and can be captured in a graph.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * splash_build_tables — give every sequence the pages that its block needs and
+ * map the block's tokens to cache slots.
+ *
+ * Sequence b holds its first page_counts[b] page-table entries. With T_b > 0 it
+ * needs ceil((context_lens[b] + T_b) / P) of them. The missing ones come off
+ * the top of the stack free_pages[0 .. *free_count - 1] in sequence order: with
+ * need_b missing pages and incl_b = need_0 + .. + need_b, sequence b is served
+ * iff incl_b <= *free_count, all of its pages or none; its i-th new page is
+ * free_pages[*free_count - 1 - (incl_b - need_b) - i]. Not served: its tokens
+ * get no slots, SPLASH_DEVICE_OUT_OF_PAGES is reported. Page-table entries
+ * below page_counts[b] and past the new ones are not written.
+ *   page_counts_out [num_seqs], free_count_out [1]: the counts after the call;
+ *     each may be its input (in place).
+ *   q_offsets [num_seqs + 1]: exclusive prefix of max(block_lens, 0).
+ *   new_offsets [num_seqs + 1]: exclusive prefix of the pages handed out;
+ *     sequence b's new entries are the last new_offsets[b+1] - new_offsets[b]
+ *     of its page_counts_out[b].
+ *   positions, slots [num_tokens]: position context_lens[b] + t and slot
+ *     page * P + position % P of row q_offsets[b] + t. Rows without a slot (of
+ *     a sequence that is not served or whose lengths are out of range, and the
+ *     rows past the last sequence of a padded batch) get slot -1, position 0.
+ * A length out of range or a sequence whose rows pass num_tokens reports
+ * SPLASH_DEVICE_BAD_LENGTH, gets no pages and no slots; the others keep their
+ * rows. A page id outside [0, num_pages) reports SPLASH_DEVICE_BAD_PAGE and
+ * maps no slot. *free_count is cut to [0, free_capacity]. num_pages * P must
+ * fit 32 bits. Page numbers only: no pool is touched.
+ */
+int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
+                        int num_tokens, int page_size, int num_pages, int32_t* page_table,
+                        int max_pages_per_seq, const int32_t* page_counts,
+                        int32_t* page_counts_out, const int32_t* free_pages, int free_capacity,
+                        const int32_t* free_count, int32_t* free_count_out, int32_t* q_offsets,
+                        int32_t* new_offsets, int32_t* positions, int32_t* slots,
+                        int* device_status, struct CUstream_st* stream);
+
+/*
+ * splash_release_pages — put the pages past ceil(keep_lens[b] / P) of every
+ * sequence back on the free list (keep_lens[b] = 0: a finished sequence; its
+ * committed length: the pages of rejected drafts; negative: nothing).
+ *
+ * The entries go behind free_pages[*free_count - 1] in sequence and position
+ * order. page_counts_out and free_count_out may be their inputs.
+ * released_offsets [num_seqs + 1]: exclusive prefix of the pages given back. A
+ * sequence whose pages do not fit free_capacity keeps them, and so does every
+ * later one that gives some back (SPLASH_DEVICE_BAD_LENGTH). The page table is
+ * only read: entries past page_counts_out[b] are stale. A page that sequences
+ * share is given back once per sequence that holds it, so shared prefixes stay
+ * inside keep_lens of all but one.
+ */
+int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* page_table,
+                         int max_pages_per_seq, int page_size, const int32_t* page_counts,
+                         int32_t* page_counts_out, int32_t* free_pages, int free_capacity,
+                         const int32_t* free_count, int32_t* free_count_out,
+                         int32_t* released_offsets, int* device_status,
+                         struct CUstream_st* stream);
+
+/*
+ * splash_qkv_append — norm and rotate the q and k heads of new tokens, write q
+ * for splash_verify_attention and quantise k and v into the cache, in one pass.
+ *
+ * q, k, v: `dtype` (SPLASH_F32 or SPLASH_BF16) [num_tokens, heads, D] with the
+ * given token and head strides in elements (a packed projection is three views
+ * of one buffer). Pointers must be 16-byte aligned and strides whole multiples
+ * of 16 bytes. Per row x of D values, everything in fp32:
+ *   q, k: x_d * w_d / sqrt(mean(x^2) + eps), with q_weight / k_weight fp32 [D];
+ *         NULL leaves that one un-normed
+ *   q, k: with R = rotary_dim (a multiple of 16, 0 for none) the first R values
+ *         are turned in pairs (u, v) = (x_i, x_{i+R/2}), or (x_2i, x_2i+1) when
+ *         `interleaved`, i < R/2, by angle a = position * inv_freq[i]:
+ *         u' = (u cos a - v sin a) * rope_scale, v' = (v cos a + u sin a) * rope_scale.
+ *         inv_freq: fp32 [R/2]. positions: int32 [num_axes, num_tokens];
+ *         frequency i uses axis freq_axis[i] (int32 [R/2], cut to the axes
+ *         there are; NULL: axis 0). Angles are exact to 2^-32 of a turn at any
+ *         32-bit position.
+ *   q:    rounded to bf16 into q_out [num_tokens, Hq, D] (contiguous; may be q
+ *         itself when q is contiguous bf16)
+ *   k, v: splash_kv_append's quantiser, into slot slots[row] (page * P +
+ *         offset, as splash_build_tables writes them)
+ * A row with a negative slot is skipped: nothing of it is written, q_out
+ * included. A slot past the pool reports SPLASH_DEVICE_BAD_PAGE and is skipped.
+ * Slots must differ. sum(x^2) must stay finite in fp32 where a norm is taken.
+ */
+int splash_qkv_append(const void* q, const void* k, const void* v, int dtype, int num_tokens,
+                      long long q_stride, long long q_head_stride, long long k_stride,
+                      long long k_head_stride, long long v_stride, long long v_head_stride,
+                      int num_q_heads, int num_kv_heads, int head_dim, const float* q_weight,
+                      const float* k_weight, float eps, const float* inv_freq,
+                      const int32_t* freq_axis, int rotary_dim, int interleaved, float rope_scale,
+                      const int32_t* positions, int num_axes, const int32_t* slots,
+                      uint16_t* q_out, int8_t* k_pages, int8_t* v_pages, float* k_scales,
+                      float* v_scales, int page_size, int num_pages, int* device_status,
+                      struct CUstream_st* stream);
+
+/*
+ * splash_kv_gather — cached rows by slot, dequantised: row i of k_out / v_out
+ * (dtype SPLASH_F32 or SPLASH_BF16, contiguous [num_rows, Hkv, D]) is
+ * the fp32 product code * scale of slots[i], rounded to dtype. With the slots of
+ * splash_build_tables this hands cached context to a dense attention. Rows with
+ * a negative slot are left as they were, a slot past the pool too
+ * (SPLASH_DEVICE_BAD_PAGE). A slot may appear more than once.
+ */
+int splash_kv_gather(const int8_t* k_pages, const int8_t* v_pages, const float* k_scales,
+                     const float* v_scales, const int32_t* slots, int num_rows, int num_kv_heads,
+                     int head_dim, int page_size, int num_pages, void* k_out, void* v_out,
+                     int dtype, int* device_status, struct CUstream_st* stream);
+
+/*
+ * Token history of the penalties: int16 [num_seqs, stride] with stride =
+ * splash_token_state_stride(vocab) (the vocabulary rounded up to 64; 0 for a
+ * vocabulary out of range). Bit 15 of entry v: v occurs in the sequence's
+ * prompt. Bits 0..14: how often it occurs in its committed output, held at
+ * 32767.
+ *
+ * splash_token_state_add — count tokens into it: rows q_offsets[b] ..
+ * q_offsets[b+1] - 1 of `tokens` belong to sequence b; with `accepted` non-NULL
+ * only the first accepted[b] + 1 of them (what splash_accept_commit commits,
+ * called before or after it). prompt != 0 sets bit 15 instead of counting.
+ * reset != 0 clears every sequence's row first, whole (a call over the rows of
+ * newly admitted sequences). Tokens outside [0, vocab) are passed over. A
+ * sequence with unusable offsets reports SPLASH_DEVICE_BAD_LENGTH.
+ * `state` is 16-byte aligned, state_stride a multiple of 64.
+ */
+int splash_token_state_stride(int vocab);
+int splash_token_state_add(const int32_t* tokens, int num_tokens, const int32_t* q_offsets,
+                           int num_seqs, const int32_t* accepted, int16_t* state,
+                           long long state_stride, int vocab, int prompt, int reset,
+                           int* device_status, struct CUstream_st* stream);
+
+/*
+ * splash_choose_targets — the target's choice after every verify token, from
+ * its logits under repetition, presence and frequency penalties, biases and
+ * grammar masks; what splash_accept_commit takes as target_tokens.
+ *
+ * logits: `dtype` (F32, BF16 or F16) [num_rows, >= vocab], row stride
+ * logits_stride elements. Rows q_offsets[b] .. q_offsets[b+1] - 1 are sequence
+ * b's verify rows (at most max_block_len <= 128 of them). For row t and token v,
+ * each step rounded to fp32, a NULL array leaving its step out:
+ *   c    = output count of v in `state` + occurrences of v among the block's
+ *          own tokens x_0 .. x_t (block_tokens), which are not committed yet
+ *   seen = c > 0, or v is in the prompt
+ *   z1 = seen ? (z > 0 ? z / repetition[b] : z * repetition[b]) : z
+ *   z2 = z1 - frequency[b] * c
+ *   z3 = c > 0 ? z2 - presence[b] : z2
+ *   z4 = z3 + bias of v: entries bias_offsets[b] .. bias_offsets[b+1] - 1 of
+ *        bias_ids / bias_values (num_bias in all); of entries with the same id
+ *        the last counts; ids outside the vocabulary are passed over
+ *   z5 = z4 where bit v % 32 of word v / 32 of the row's mask is 1, else -inf.
+ *        mask: int32 [num_masks, mask_stride words]. Row i uses mask
+ *        mask_rows[i] (-1: no mask), or mask i when mask_rows is NULL. An index
+ *        past num_masks allows nothing (SPLASH_DEVICE_BAD_LENGTH).
+ * repetition values must be > 0 and finite (others count as 1), frequency and
+ * presence finite.
+ * target_tokens[i]: the lowest v with the largest z5 above -inf; -1 where there
+ * is none. NaN is never chosen.
+ * out (NULL: not written): fp32 z5 [num_rows, vocab], row stride out_stride; may
+ * be the logits themselves (F32, same stride).
+ * Rows of no sequence, and of sequences with unusable offsets
+ * (SPLASH_DEVICE_BAD_LENGTH), are left as they were. The workspace (256-byte
+ * aligned) is scratch for the duration of the call.
+ */
+size_t splash_choose_targets_workspace_size(int num_rows, int vocab);
+int splash_choose_targets(const void* logits, int dtype, long long logits_stride, int num_rows,
+                          int vocab, const int32_t* q_offsets, int num_seqs, int max_block_len,
+                          const int32_t* block_tokens, const int16_t* state,
+                          long long state_stride, const float* repetition, const float* presence,
+                          const float* frequency, const int32_t* bias_offsets,
+                          const int32_t* bias_ids, const float* bias_values, int num_bias,
+                          const int32_t* mask, long long mask_stride, int num_masks,
+                          const int32_t* mask_rows, float* out, long long out_stride,
+                          int32_t* target_tokens, void* workspace, size_t workspace_bytes,
+                          int* device_status, struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,7 @@
 
 #include "splash_common.cuh"
 #include "splash_groups.cuh"
+#include "splash_host.cuh"
 
 namespace splash {
 cudaError_t launch_kv_append(const float*, const float*, int, int8_t*, int8_t*, float*, float*,
@@ -36,8 +37,6 @@ cudaError_t launch_verify_tt(const AttnParams&, const CUtensorMap&, int, cudaStr
 constexpr int kSimtTile = 64;
 constexpr int kTcTile = 64;
 
-namespace {
-
 int device_sm_count() {
   static std::mutex mu;
   static int cache[64] = {0};
@@ -52,16 +51,13 @@ int device_sm_count() {
   return cache[dev];
 }
 
+namespace {
+
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;   // 1 s
 std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitNs};
 std::atomic<unsigned long long> g_launches{0};               // kernels enqueued so far
-
-cudaError_t counted(cudaError_t e) {
-  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
-}
 
 // CTAs per class: the tensor-core kernel runs one CTA per SM, the CUDA-core
 // kernel as many as fit.
@@ -81,6 +77,12 @@ long long rows_bound_for(int num_q_tokens, int num_q_heads, int rows_cap, int nc
 }
 
 }  // namespace
+
+cudaError_t counted(cudaError_t e) {
+  if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
 }  // namespace splash
 
 using namespace splash;
