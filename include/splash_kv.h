@@ -472,8 +472,8 @@ int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* 
  *
  * q, k, v: `dtype` (SPLASH_F32 or SPLASH_BF16) [num_tokens, heads, D] with the
  * given token and head strides in elements (a packed projection is three views
- * of one buffer). Pointers must be 16-byte aligned and strides whole multiples
- * of 16 bytes. Per row x of D values, everything in fp32:
+ * of one buffer). Row, weight and pool pointers must be 16-byte aligned and
+ * strides whole multiples of 16 bytes. Per row x of D values, everything in fp32:
  *   q, k: x_d * w_d / sqrt(mean(x^2) + eps), with q_weight / k_weight fp32 [D];
  *         NULL leaves that one un-normed
  *   q, k: with R = rotary_dim (a multiple of 16, 0 for none) the first R values

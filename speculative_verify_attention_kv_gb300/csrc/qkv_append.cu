@@ -19,12 +19,23 @@
 // here). sincospif then needs no range reduction.
 //
 // A warp takes one token and a run of its heads, 8 values a lane (so a head of
-// D values takes D/8 lanes, and a warp 256/D heads at once). A lane's column is
-// the same for every head, so the token's 8 cosines and sines, the norm weights
-// and the frequencies stay in registers, and there is neither shared memory nor
-// a barrier. Loads of kBatch head rows are in flight while the angles are
-// computed. Few tokens are split over more warps by heads (rows_per_item).
+// D values takes D/8 lanes, and a warp 256/D heads at once). The 8 values are two
+// pieces of 4 columns, chosen so that both halves of a rotated pair sit in one
+// lane: columns 4l.. and R/2 + 4l.. (interleaved: 8 columns in a row). So the
+// rotation needs no exchange between lanes, a lane has 4 angles for the token,
+// the same for every head, and the cosines, sines, norm weights and frequencies
+// stay in registers: no shared memory, no barrier.
+//
+// By its bytes it is bound by HBM, but with 8192 values to a 16 KB token the
+// instructions come close, so they are what the layout saves. Products run on
+// pairs of fp32 (f32x2); the weight is folded into the token's cosines and sines.
+// A batch of kB head rows is worked on together: their kB sums of squares are
+// reduced in one exchange pattern (6 shuffles and one root for 4 rows instead of
+// 20 and 4), and the next batch's loads, of the next token at the end, are in
+// flight meanwhile. A batch is all of one kind (q, k or v). Few tokens are split
+// over more warps by batches.
 #include <cmath>
+#include <type_traits>
 
 #include "splash_common.cuh"
 #include "splash_host.cuh"
@@ -37,7 +48,10 @@ namespace {
 constexpr int kQkvWarps = 4;
 constexpr int kQkvThreads = 32 * kQkvWarps;
 constexpr int kEpl = 8;          // values a lane holds of a head row
-constexpr int kBatch = 4;        // head rows in flight per lane
+constexpr int kWarpsPerSm = 16;  // resident: what the registers leave room for
+// Head rows of a batch: 64 bytes a lane in flight
+template <typename T>
+constexpr int kBatch = 8 / sizeof(T);
 
 struct QkvParams {
   const void* q;
@@ -62,21 +76,29 @@ struct QkvParams {
   float* k_scales;
   float* v_scales;
   int num_pages;
-  int groups_per_item;           // warp-wide row groups an item handles
+  int batches_per_item;          // batches of head rows an item handles
   int items_per_token;
   int* status;
 };
 
-// Raw 8 values of a row: 16 bytes of bf16, 32 of fp32.
+// A lane's 8 values of a row as they are stored: two pieces of 4.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
-  uint4 a;
-  __device__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  uint2 a, b;
+  __device__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a = *reinterpret_cast<const uint2*>(p);
+    b = *reinterpret_cast<const uint2*>(q);
+  }
+  __device__ void load8(const __nv_bfloat16* p) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    a = make_uint2(w.x, w.y);
+    b = make_uint2(w.z, w.w);
+  }
+  __device__ void zero() { a = b = make_uint2(0, 0); }
   __device__ void get(float (&x)[kEpl]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -87,16 +109,22 @@ struct Raw<__nv_bfloat16> {
 template <>
 struct Raw<float> {
   float4 a, b;
-  __device__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  __device__ void load(const float* p, const float* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
   }
+  __device__ void load8(const float* p) { load(p, p + 4); }
   __device__ void zero() { a = b = make_float4(0, 0, 0, 0); }
   __device__ void get(float (&x)[kEpl]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
 };
+
+__device__ inline uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
 
 // f / (2 pi) turns as a 64-bit fraction of a turn (whole turns drop out).
 __device__ inline unsigned long long turns64(float f) {
@@ -117,164 +145,295 @@ __device__ inline unsigned long long turns64(float f) {
   return bits >> 31 ? 0ull - r : r;
 }
 
-template <int D, typename TIn>
-__global__ void __launch_bounds__(kQkvThreads) qkv_append_kernel(QkvParams p) {
-  constexpr int kLanes = D / kEpl;               // lanes of a head row
-  constexpr int kRows = 32 / kLanes;             // head rows of a warp-wide group
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
-  const int tok = (int)(item / p.items_per_token);
-  if (tok >= p.n) return;
-  const int part = (int)(item % p.items_per_token);
-  const int slot = p.slots[tok];
-  if (slot < 0) return;                          // a padded row: nothing is written
-  const int page = slot / kPageSize;
-  if (page >= p.num_pages) {
-    if (lane == 0) report(p.status, SPLASH_DEVICE_BAD_PAGE);
-    return;
+// Sums v[i] over the kLanes lanes of a head row, for kB rows at once, and takes
+// f(sum) of each: every step halves the values that a lane carries, the last ones
+// carry one; f is computed once, and each row's result handed back to all lanes.
+template <int kB, int kLanes, typename F>
+__device__ inline void reduce_rows(float (&v)[kB], int lane, F f) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  static_assert(kB == 2 || kB == 4, "rows of a batch");
+  constexpr int h1 = kLanes / 2, h2 = kLanes / 4;
+  const bool up = lane & h1;
+  float a = (up ? v[1] : v[0]) + __shfl_xor_sync(kAll, up ? v[0] : v[1], h1);
+  if constexpr (kB == 4) {
+    const float b = (up ? v[3] : v[2]) + __shfl_xor_sync(kAll, up ? v[2] : v[3], h1);
+    const bool up2 = lane & h2;
+    a = (up2 ? b : a) + __shfl_xor_sync(kAll, up2 ? a : b, h2);
   }
-  const int col = (lane % kLanes) * kEpl;
-  const int rows = p.hq + 2 * p.hkv;
-  const int g0 = part * p.groups_per_item;
-  const int g1 = min(g0 + p.groups_per_item, (rows + kRows - 1) / kRows);
+#pragma unroll
+  for (int o = kB == 4 ? kLanes / 8 : h2; o > 0; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
+  a = f(a);
+  const int row0 = lane & ~(kLanes - 1);         // first lane of this lane's head row
+#pragma unroll
+  for (int i = 0; i < kB; ++i)
+    v[i] = __shfl_sync(kAll, a, row0 + (i & 1 ? h1 : 0) + (i & 2 ? h2 : 0));
+}
 
-  auto load = [&](Raw<TIn>& raw, int r) {
-    if (r >= rows) {
-      raw.zero();
-    } else if (r < p.hq) {
-      raw.load(static_cast<const TIn*>(p.q) + tok * p.q_tok + r * p.q_head + col);
-    } else if (r < p.hq + p.hkv) {
-      raw.load(static_cast<const TIn*>(p.k) + tok * p.k_tok + (r - p.hq) * p.k_head + col);
+// kPaired: interleaved pairs. Values are held as x[0..1] = u, x[2..3] = v of the
+// lane's pairs (in column order where the lane's columns are not rotated and
+// kPaired is false: then u is the first piece, v the second).
+template <int D, typename TIn, bool kPaired>
+__global__ void __launch_bounds__(kQkvThreads, kWarpsPerSm / kQkvWarps)
+qkv_append_kernel(QkvParams p) {
+  constexpr int kLanes = D / kEpl;               // lanes of a head row
+  constexpr int kRows = 32 / kLanes;             // head rows of a warp-wide load
+  constexpr int kB = kBatch<TIn>;
+  constexpr int kHeads = kB * kRows;             // heads of a batch
+  const int lane = threadIdx.x & 31, l = lane % kLanes, hl = lane / kLanes;
+  const int nq = (p.hq + kHeads - 1) / kHeads, nk = (p.hkv + kHeads - 1) / kHeads;
+  const int quads = p.half / 4;                  // pieces of half the rotated columns
+  const bool turns = l < quads;                  // at most D/8 of them
+  const int ca = kPaired ? 8 * l : (turns ? 4 * l : 8 * l);
+  const int cb = kPaired ? ca + 4 : (turns ? p.half + 4 * l : ca + 4);
+
+  // What a lane keeps for all tokens: its frequencies in turns, and its columns
+  // of the norm weights in the order of x.
+  unsigned long long turn[4];
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn[i] = turns64(p.inv_freq[4 * l + i]);
+  }
+  auto weights = [&](const float* w, F2 (&out)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(w + ca), b = *reinterpret_cast<const float4*>(w + cb);
+    if constexpr (kPaired) {
+      out[0] = f2(a.x, a.z); out[1] = f2(b.x, b.z);
+      out[2] = f2(a.y, a.w); out[3] = f2(b.y, b.w);
     } else {
-      raw.load(static_cast<const TIn*>(p.v) + tok * p.v_tok + (r - p.hq - p.hkv) * p.v_head + col);
+      out[0] = f2(a.x, a.y); out[1] = f2(a.z, a.w);
+      out[2] = f2(b.x, b.y); out[3] = f2(b.z, b.w);
     }
   };
 
-  Raw<TIn> raw[kBatch];
+  // Batch `bi` of token `tok`: rows past the last head are zero.
+  auto load = [&](Raw<TIn> (&raw)[kB], int tok, int bi) {
+    const TIn* base;
+    long long head;
+    int h0, heads;
+    if (bi < nq) {
+      h0 = bi * kHeads; heads = p.hq; head = p.q_head;
+      base = static_cast<const TIn*>(p.q) + tok * p.q_tok;
+    } else if (bi < nq + nk) {
+      h0 = (bi - nq) * kHeads; heads = p.hkv; head = p.k_head;
+      base = static_cast<const TIn*>(p.k) + tok * p.k_tok;
+    } else {
+      h0 = (bi - nq - nk) * kHeads; heads = p.hkv; head = p.v_head;
+      base = static_cast<const TIn*>(p.v) + tok * p.v_tok;
+    }
+    const TIn* row = base + (h0 + hl) * head;
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u)
-    if (g0 + u < g1) load(raw[u], (g0 + u) * kRows + lane / kLanes);
+    for (int u = 0; u < kB; ++u) {
+      if (h0 + u * kRows + hl >= heads) raw[u].zero();
+      else if constexpr (kPaired) raw[u].load8(row + ca);
+      else raw[u].load(row + ca, row + cb);
+      row += kRows * head;
+    }
+  };
 
-  // This lane's columns of the rotation: x' = x * cs + partner * sn.
-  const bool paired = p.half < 0;
-  const int half = paired ? -p.half : p.half;
-  const bool turns = col < 2 * half;
-  float cs[kEpl], sn[kEpl];
-  if (turns) {
-    const int f0 = paired ? col / 2 : (col < half ? col : col - half);
-    const int nf = paired ? kEpl / 2 : kEpl;
-    const int pos0 = p.positions[tok];
+  const unsigned per_token = p.items_per_token, items = p.n * per_token;
+  const unsigned step = gridDim.x * kQkvWarps;
+  auto token_of = [&](unsigned item) { return (int)(per_token == 1 ? item : item / per_token); };
+  auto batch_of = [&](unsigned item) {
+    return per_token == 1 ? 0 : (int)(item % per_token) * p.batches_per_item;
+  };
+  unsigned item = blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
+  Raw<TIn> raw[kB];
+  if (item < items) load(raw, token_of(item), batch_of(item));
+
+  for (; item < items; item += step) {
+    const int tok = token_of(item), b0 = batch_of(item);
+    const int b1 = min(b0 + p.batches_per_item, nq + 2 * nk);
+    const int slot = p.slots[tok];
+    const int page = slot / kPageSize, at = slot % kPageSize;
+    // the batch after `bi`, of the next item at the end of this one
+    auto load_after = [&](int bi) {
+      const unsigned next = item + step;
+      if (bi + 1 < b1) load(raw, tok, bi + 1);
+      else if (next < items) load(raw, token_of(next), batch_of(next));
+    };
+    if (slot < 0 || page >= p.num_pages) {       // a padded row: nothing is written
+      if (slot >= 0 && lane == 0) report(p.status, SPLASH_DEVICE_BAD_PAGE);
+      load_after(b1);
+      continue;
+    }
+
+    // u' = u c - v s, v' = v c + u s for the lane's four pairs
+    F2 cs[2], sn[2];
+    if (turns) {
+      float c[4], s[4];
+      const int pos0 = p.positions[tok];
 #pragma unroll
-    for (int i = 0; i < kEpl; ++i) {
-      if (i < nf) {
+      for (int i = 0; i < 4; ++i) {
         int pos = pos0;
         if (p.freq_axis) {
-          const int a = max(0, min(p.freq_axis[f0 + i], p.axes - 1));
+          const int a = max(0, min(p.freq_axis[4 * l + i], p.axes - 1));
           pos = p.positions[(size_t)a * p.n + tok];
         }
-        const unsigned long long ph = (unsigned long long)(long long)pos * turns64(p.inv_freq[f0 + i]);
+        const unsigned long long ph = (unsigned long long)(long long)pos * turn[i];
         // signed 32-bit fraction of a turn -> half turns in [-1, 1)
-        const float x = (float)(int)(ph >> 32) * 4.656612873077393e-10f;
-        float s, c;
-        sincospif(x, &s, &c);
-        cs[i] = c * p.rope_scale;
-        sn[i] = s * p.rope_scale;
+        sincospif((float)(int)(ph >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);
+        c[i] *= p.rope_scale;
+        s[i] *= p.rope_scale;
       }
+      cs[0] = f2(c[0], c[1]); cs[1] = f2(c[2], c[3]);
+      sn[0] = f2(s[0], s[1]); sn[1] = f2(s[2], s[3]);
     }
-    if (paired) {
+    // With weights w = (a, b): u' = u (a c) - v (b s), v' = v (b c) + u (a s); where
+    // nothing turns, u' = u a, v' = v b in co[0..1] and co[2..3].
+    F2 co[8];                                    // a c, b c, -b s, a s, two pairs each
+    auto coefficients = [&](const float* weight) {
+      const F2 neg = f2(-1.f, -1.f);
+      F2 w[4];
+      if (weight) weights(weight, w);
 #pragma unroll
-      for (int i = kEpl / 2 - 1; i >= 0; --i) {
-        cs[2 * i + 1] = cs[2 * i] = cs[i];
-        sn[2 * i + 1] = sn[i];
-        sn[2 * i] = -sn[2 * i + 1];
+      for (int i = 0; i < 2; ++i) {
+        if (turns) {
+          co[i] = weight ? mul2(w[i], cs[i]) : cs[i];
+          co[2 + i] = weight ? mul2(w[2 + i], cs[i]) : cs[i];
+          co[4 + i] = mul2(weight ? mul2(w[2 + i], sn[i]) : sn[i], neg);
+          co[6 + i] = weight ? mul2(w[i], sn[i]) : sn[i];
+        } else if (weight) {
+          co[i] = w[i];
+          co[2 + i] = w[2 + i];
+        }
       }
-    } else if (col < half) {
-#pragma unroll
-      for (int i = 0; i < kEpl; ++i) sn[i] = -sn[i];
-    }
-  }
-  const int from = paired || !turns ? lane : (col < half ? lane + half / kEpl : lane - half / kEpl);
-  float qw[kEpl], kw[kEpl];
-  if (p.q_weight) {
-#pragma unroll
-    for (int i = 0; i < kEpl; ++i) qw[i] = p.q_weight[col + i];
-  }
-  if (p.k_weight) {
-#pragma unroll
-    for (int i = 0; i < kEpl; ++i) kw[i] = p.k_weight[col + i];
-  }
+    };
 
-  for (int g = g0; g < g1; g += kBatch) {
+    // One batch; `kv` (a compile-time truth value): k or v. turned: norm and rotate.
+    auto process = [&](auto kv, int bi, int h0, bool turned, const float* weight, auto* out_row,
+                       float* scale) {
+      constexpr bool kKv = decltype(kv)::value;
+      F2 x[kB][4];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (g + u >= g1) break;
-      const int r = (g + u) * kRows + lane / kLanes;
-      const bool is_q = r < p.hq, is_k = !is_q && r < p.hq + p.hkv, live = r < rows;
-      float x[kEpl];
-      raw[u].get(x);
-      if (g + u + kBatch < g1) load(raw[u], r + kBatch * kRows);
-      if (p.q_weight || p.k_weight) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < kEpl; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-        if (is_q && p.q_weight) {
-#pragma unroll
-          for (int i = 0; i < kEpl; ++i) x[i] = x[i] * rn * qw[i];
-        } else if (is_k && p.k_weight) {
-#pragma unroll
-          for (int i = 0; i < kEpl; ++i) x[i] = x[i] * rn * kw[i];
-        }
-      }
-      if (half > 0) {
+      for (int u = 0; u < kB; ++u) {
         float y[kEpl];
-        if (paired) {
-#pragma unroll
-          for (int i = 0; i < kEpl; ++i) y[i] = x[i ^ 1];
+        raw[u].get(y);
+        if constexpr (kPaired) {
+          x[u][0] = f2(y[0], y[2]); x[u][1] = f2(y[4], y[6]);
+          x[u][2] = f2(y[1], y[3]); x[u][3] = f2(y[5], y[7]);
         } else {
-#pragma unroll
-          for (int i = 0; i < kEpl; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
-        }
-        if (turns && (is_q || is_k)) {
-#pragma unroll
-          for (int i = 0; i < kEpl; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
+          x[u][0] = f2(y[0], y[1]); x[u][1] = f2(y[2], y[3]);
+          x[u][2] = f2(y[4], y[5]); x[u][3] = f2(y[6], y[7]);
         }
       }
-      if (__any_sync(0xffffffffu, live && !is_q)) {
-        float a = 0.f;
+      load_after(bi);
+      if (turned) {
+        float ss[kB];
+        if (weight) {
 #pragma unroll
-        for (int i = 0; i < kEpl; ++i) a = fmaxf(a, fabsf(x[i]));
+          for (int u = 0; u < kB; ++u) {
+            F2 sq = mul2(x[u][0], x[u][0]);
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (live && !is_q) {
-          const int h = is_k ? r - p.hq : r - p.hq - p.hkv;
-          const int at = slot % kPageSize;
-          int8_t* codes = (is_k ? p.k_pages : p.v_pages) + code_offset(page, h, p.hkv, at, D) + col;
-          float* scale = (is_k ? p.k_scales : p.v_scales) + ((size_t)page * p.hkv + h) * kPageSize + at;
-          store_codes<kEpl>(x, a, codes, scale, col == 0);
+            for (int i = 1; i < 4; ++i) sq = fma2(x[u][i], x[u][i], sq);
+            float s1;
+            split(sq, ss[u], s1);
+            ss[u] += s1;
+          }
+          reduce_rows<kB, kLanes>(ss, lane, [&](float t) { return rsqrtf(t * (1.f / D) + p.eps); });
+        }
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+          if (turns) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const F2 a = x[u][i], b = x[u][2 + i];
+              x[u][i] = fma2(b, co[4 + i], mul2(a, co[i]));
+              x[u][2 + i] = fma2(a, co[6 + i], mul2(b, co[2 + i]));
+            }
+          } else if (weight) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], co[i]);
+          }
+          if (weight) {
+            const F2 rn = f2(ss[u], ss[u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], rn);
+          }
         }
       }
-      if (is_q) {
-        uint4 w;
-        __nv_bfloat162 t;
-        t = __floats2bfloat162_rn(x[0], x[1]); w.x = *reinterpret_cast<uint32_t*>(&t);
-        t = __floats2bfloat162_rn(x[2], x[3]); w.y = *reinterpret_cast<uint32_t*>(&t);
-        t = __floats2bfloat162_rn(x[4], x[5]); w.z = *reinterpret_cast<uint32_t*>(&t);
-        t = __floats2bfloat162_rn(x[6], x[7]); w.w = *reinterpret_cast<uint32_t*>(&t);
-        *reinterpret_cast<uint4*>(p.q_out + ((size_t)tok * p.hq + r) * D + col) = w;
+      const int heads = kKv ? p.hkv : p.hq;
+      auto* out_b = out_row + (cb - ca);
+#pragma unroll
+      for (int u = 0; u < kB; ++u) {
+        if (h0 + u * kRows >= heads) break;
+        const bool live = h0 + u * kRows + hl < heads;
+        float y[kEpl];                           // back to column order
+        if constexpr (kPaired) {
+          split(x[u][0], y[0], y[2]); split(x[u][1], y[4], y[6]);
+          split(x[u][2], y[1], y[3]); split(x[u][3], y[5], y[7]);
+        } else {
+          split(x[u][0], y[0], y[1]); split(x[u][1], y[2], y[3]);
+          split(x[u][2], y[4], y[5]); split(x[u][3], y[6], y[7]);
+        }
+        if constexpr (!kKv) {
+          constexpr int kNext = kRows * D;       // values between the heads of a lane
+          const uint32_t w0 = bf16_pair(y[0], y[1]), w1 = bf16_pair(y[2], y[3]);
+          const uint32_t w2 = bf16_pair(y[4], y[5]), w3 = bf16_pair(y[6], y[7]);
+          if (live) {
+            if constexpr (kPaired) {
+              *reinterpret_cast<uint4*>(out_row + u * kNext) = make_uint4(w0, w1, w2, w3);
+            } else {
+              *reinterpret_cast<uint2*>(out_row + u * kNext) = make_uint2(w0, w1);
+              *reinterpret_cast<uint2*>(out_b + u * kNext) = make_uint2(w2, w3);
+            }
+          }
+        } else {
+          constexpr int kNext = kRows * 2 * kPageSize * D;
+          float a = 0.f;
+#pragma unroll
+          for (int i = 0; i < kEpl; ++i) a = fmaxf(a, fabsf(y[i]));
+          if constexpr (kLanes == 32) {          // the order of fp32 >= 0 is that of its bits
+            a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+          } else {
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          }
+          const float s = __fdiv_rn(a, 127.0f);
+          uint32_t packed[2];
+          quantise<kEpl>(y, s, packed);
+          if (live) {
+            if constexpr (kPaired) {
+              *reinterpret_cast<uint2*>(out_row + u * kNext) = make_uint2(packed[0], packed[1]);
+            } else {
+              *reinterpret_cast<uint32_t*>(out_row + u * kNext) = packed[0];
+              *reinterpret_cast<uint32_t*>(out_b + u * kNext) = packed[1];
+            }
+            if (l == 0) scale[u * kRows * kPageSize] = s;
+          }
+        }
       }
+    };
+
+    int bi = b0;
+    if (bi < min(b1, nq)) {
+      coefficients(p.q_weight);
+      for (; bi < min(b1, nq); ++bi)
+        process(std::false_type{}, bi, bi * kHeads, true, p.q_weight,
+                p.q_out + ((size_t)tok * p.hq + bi * kHeads + hl) * D + ca, nullptr);
+    }
+    if (bi < min(b1, nq + nk)) coefficients(p.k_weight);
+    for (; bi < b1; ++bi) {
+      const bool is_k = bi < nq + nk;
+      const int h0 = (is_k ? bi - nq : bi - nq - nk) * kHeads, h = h0 + hl;
+      process(std::true_type{}, bi, h0, is_k, p.k_weight,
+              (is_k ? p.k_pages : p.v_pages) + code_offset(page, h, p.hkv, at, D) + ca,
+              (is_k ? p.k_scales : p.v_scales) + ((size_t)page * p.hkv + h) * kPageSize + at);
     }
   }
 }
 
-template <int D>
+template <int D, bool kPaired>
 cudaError_t launch_qkv(const QkvParams& p, int dtype, unsigned grid, cudaStream_t s) {
-  if (dtype == SPLASH_F32) qkv_append_kernel<D, float><<<grid, kQkvThreads, 0, s>>>(p);
-  else qkv_append_kernel<D, __nv_bfloat16><<<grid, kQkvThreads, 0, s>>>(p);
+  if (dtype == SPLASH_F32)
+    qkv_append_kernel<D, float, kPaired><<<grid, kQkvThreads, 0, s>>>(p);
+  else
+    qkv_append_kernel<D, __nv_bfloat16, kPaired><<<grid, kQkvThreads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_qkv(const QkvParams& p, int dtype, bool paired, unsigned grid, cudaStream_t s) {
+  return paired ? launch_qkv<D, true>(p, dtype, grid, s) : launch_qkv<D, false>(p, dtype, grid, s);
 }
 
 }  // namespace
@@ -309,7 +468,7 @@ extern "C" int splash_qkv_append(
   const int per16 = dtype == SPLASH_F32 ? 4 : 8;
   const long long strides = q_stride | q_head_stride | k_stride | k_head_stride | v_stride | v_head_stride;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_pages) ||
-      strides < 0 || strides % per16)
+      !aligned16(q_weight) || !aligned16(k_weight) || strides < 0 || strides % per16)
     return SPLASH_ERR_INVALID_ARGUMENT;
 
   QkvParams p{};
@@ -321,7 +480,7 @@ extern "C" int splash_qkv_append(
   p.hq = num_q_heads; p.hkv = num_kv_heads;
   p.q_weight = q_weight; p.k_weight = k_weight; p.eps = eps;
   p.inv_freq = inv_freq; p.freq_axis = freq_axis;
-  p.half = interleaved ? -(rotary_dim / 2) : rotary_dim / 2;
+  p.half = rotary_dim / 2;
   p.positions = positions; p.axes = num_axes; p.rope_scale = rope_scale;
   p.slots = slots;
   p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
@@ -331,24 +490,25 @@ extern "C" int splash_qkv_append(
 
   const int sms = device_sm_count();
   if (sms <= 0) return SPLASH_ERR_CUDA;
-  const int rows_per_group = 32 * kEpl / head_dim;
-  const int groups = (num_q_heads + 2 * num_kv_heads + rows_per_group - 1) / rows_per_group;
-  // A token's heads stay with one warp while there are warps enough to fill the
-  // GPU; fewer tokens are split by heads.
-  const long long warps = 32LL * sms;
-  int per_item = (int)((groups * (long long)num_tokens + warps - 1) / warps);
-  per_item = per_item < 1 ? 1 : (per_item > groups ? groups : per_item);
-  p.groups_per_item = per_item;
-  p.items_per_token = (groups + per_item - 1) / per_item;
+  const int heads = (dtype == SPLASH_F32 ? kBatch<float> : kBatch<__nv_bfloat16>) * (32 * kEpl / head_dim);
+  const int batches = (num_q_heads + heads - 1) / heads + 2 * ((num_kv_heads + heads - 1) / heads);
+  // A token's heads stay with one warp while there are tokens enough to fill the
+  // GPU; fewer are split by batches. More items than warps fit at once are taken
+  // in turns, so that the frequencies are set up once a warp.
+  const long long warps = (long long)kWarpsPerSm * sms;
+  int per_item = (int)((batches * (long long)num_tokens + warps - 1) / warps);
+  per_item = per_item < 1 ? 1 : (per_item > batches ? batches : per_item);
+  p.batches_per_item = per_item;
+  p.items_per_token = (batches + per_item - 1) / per_item;
   const long long items = (long long)p.items_per_token * num_tokens;
-  const long long ctas = (items + kQkvWarps - 1) / kQkvWarps;
-  if (ctas > 0x7fffffffLL) return SPLASH_ERR_UNSUPPORTED;
+  const long long want = (items + kQkvWarps - 1) / kQkvWarps, most = warps / kQkvWarps;
+  const unsigned grid = (unsigned)(want < most ? want : most);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (head_dim) {
-    case 64: e = launch_qkv<64>(p, dtype, (unsigned)ctas, s); break;
-    case 128: e = launch_qkv<128>(p, dtype, (unsigned)ctas, s); break;
-    default: e = launch_qkv<256>(p, dtype, (unsigned)ctas, s); break;
+    case 64: e = launch_qkv<64>(p, dtype, interleaved != 0, grid, s); break;
+    case 128: e = launch_qkv<128>(p, dtype, interleaved != 0, grid, s); break;
+    default: e = launch_qkv<256>(p, dtype, interleaved != 0, grid, s); break;
   }
   return counted(e) == cudaSuccess ? SPLASH_OK : SPLASH_ERR_CUDA;
 }

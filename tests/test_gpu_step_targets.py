@@ -162,10 +162,11 @@ def test_many_sequences_and_long_blocks(kind):
     s.check()
 
 
-def test_windows_of_two_vectors():
-    """Sequences times windows enough that a thread takes two vectors."""
-    for kind, V in (("bf16", 40001), ("f32", 20480)):
-        s = Scene(V, [1, 2] * 40, V, kind, masks="some", dense_state=0.01, nbias=300)
+def test_windows_of_several_vectors():
+    """Sequences times windows enough that a thread takes two or four vectors."""
+    for kind, V, B in (("bf16", 40001, 80), ("bf16", 50003, 80), ("f16", 49152, 80),
+                       ("f32", 20480, 80), ("f32", 16389, 60)):
+        s = Scene(V, [1, 2] * (B // 2), V, kind, masks="some", dense_state=0.01, nbias=300)
         s.check(out="new")
         s.check(out=None)
 
