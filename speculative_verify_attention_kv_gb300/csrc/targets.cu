@@ -15,22 +15,27 @@
 // each step rounded to fp32. The choice is the lowest index of the largest z5
 // above -inf (NaN is never chosen), -1 where there is none.
 //
-// What bounds it is reading the logits once. Of a vocabulary only few tokens are
-// touched by a penalty or a bias, so the work is split in two. A CTA takes a
-// window of the vocabulary for up to kChunk rows of one sequence. It first marks
-// the touched ("special") tokens of the window in a bitmap from the state, the
-// block and the biases, all read once for the rows. The dense pass then streams
-// the rows, the next ones' loads in flight, and takes only a maximum, of the logits as they are stored:
-// excluded tokens (special ones, and those that the mask closes) become -inf by
-// one logic operation a register, 16-bit types stay packed in pairs. One warp
-// maximum a row tells which warp's stretch holds the window's best; its place is
-// looked up once at the end. The special tokens (a few dozen a window) are done
-// exactly, one a lane for a few rows at a time. Choices are 64-bit keys (ordered
-// value, complement of the index) merged by maximum, which no order changes. A
-// second kernel takes each row's maximum over the windows.
+// What bounds it is reading the logits once; next to that, latency, since a
+// step's rows are few and everything before the logits (offsets, state, biases,
+// masks) is a chain of loads. So a warp works for itself, without block barriers:
+// it takes a run of segments of the vocabulary (1024 tokens) for up to kChunk rows
+// of a sequence, and the next row's or segment's loads are in flight while it works
+// on one. Of a segment only few tokens are
+// touched by a penalty or a bias ("special"). It marks them in a bitmap, then
+//   - streams the rows and takes only a maximum, of the logits as they are stored:
+//     excluded tokens (special ones, and those that the mask closes) become -inf
+//     by one logic operation a register, 16-bit types stay packed in pairs, and
+//     the place of a maximum is looked up only where it beats the run's best;
+//   - does the special tokens exactly, a token a lane; the loads of the first 32
+//     of them run under the dense pass.
+// Choices are 64-bit keys (ordered value, complement of the index) merged by
+// maximum, which no order changes; a second kernel takes each row's maximum over
+// its runs. A CTA per window with block barriers, tried before in three forms,
+// took 33 us and more for 16 x 16 rows of 131072 bf16 logits; see the measured
+// figures at the launch.
 //
 // Rows of an odd vocabulary start at any alignment. Each row's vector grid is
-// shifted to its own 16-byte boundary and its window with it, so the loads stay
+// shifted to its own 16-byte boundary and its segments with it, so the loads stay
 // full vectors; the bitmap and mask bits of a vector come from a funnel shift.
 #include <climits>
 #include <cmath>
@@ -43,13 +48,14 @@ namespace splash {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // of the history kernels
 constexpr int kMaxBlock = 128;       // verify rows of a sequence
-// Rows of a CTA: enough to share a window's set-up, few enough that sequences of
-// long and short blocks end together and that few sequences fill the GPU.
-constexpr int kChunk = 8;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRowBatch = 4;         // rows a special token is done for at once
+// Rows of a warp: enough to share a segment's set-up, few enough that sequences
+// of long and short blocks end together and that few sequences fill the GPU.
+constexpr int kChunk = 4;
+constexpr int kWarpsPerCta = 4;
+// Warps beyond which segments are taken in turn, for each SM
+constexpr long long kWarpsPerSm = 64;
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct TargetParams {
@@ -77,8 +83,10 @@ struct TargetParams {
   float* out;                        // may be the logits (fp32, same stride)
   long long out_stride;
   int32_t* targets;
-  unsigned long long* part;          // [num_rows, windows]
-  int windows;
+  unsigned long long* part;          // [num_rows, runs]
+  int segments;                      // of a row
+  int span;                          // segments of a run
+  int runs;
   int chunks;                        // of kChunk rows, to max_block
   int* status;
 };
@@ -92,10 +100,10 @@ __device__ inline float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat1
 template <>
 __device__ inline float widen<__half>(__half v) { return __half2float(v); }
 
-// 16 bytes of logits as they are stored, and the few operations the dense pass
-// needs on them. `keep` has a bit per value; a value whose bit is 0 becomes -inf.
-// A bit is spread over its value's bytes by a product that brings bit j to the
-// top of byte j, and a byte permute that repeats the sign of a byte.
+// Eight logits as they are stored, and the few operations the dense pass needs on
+// them. `keep` has a bit per value; a value whose bit is 0 becomes -inf. A bit is
+// spread over its value's bytes by a product that brings bit j to the top of byte
+// j, and a byte permute that repeats the sign of a byte.
 __device__ inline uint32_t spread4(uint32_t bits) { return (bits & 15u) * 0x10204080u; }
 template <uint32_t kSel>
 __device__ inline uint32_t signs(uint32_t w) {         // a selector nibble 8 + b: sign of byte b
@@ -108,72 +116,82 @@ __device__ inline uint32_t keep_or(uint32_t w, uint32_t m, uint32_t other) {
 }
 
 template <typename T>
-struct Packed;
+struct Octet;
 template <>
-struct Packed<float> {
+struct Octet<float> {
+  uint4 a, b;
   static constexpr uint32_t kNone = 0xff800000u;      // -inf
-  __device__ static void drop(uint4& w, uint32_t keep) {
+  __device__ void load(const float* z) {
+    a = reinterpret_cast<const uint4*>(z)[0];
+    b = reinterpret_cast<const uint4*>(z)[1];
+  }
+  __device__ static void drop4(uint4& w, uint32_t keep) {
     const uint32_t s = spread4(keep);
     w.x = keep_or(w.x, signs<0x8888>(s), kNone);
     w.y = keep_or(w.y, signs<0x9999>(s), kNone);
     w.z = keep_or(w.z, signs<0xaaaa>(s), kNone);
     w.w = keep_or(w.w, signs<0xbbbb>(s), kNone);
   }
-  __device__ static uint32_t none() { return kNone; }
-  __device__ static uint32_t max(uint32_t m, const uint4& w) {       // a NaN loses
-    const float a = fmaxf(fmaxf(__uint_as_float(m), __uint_as_float(w.x)), __uint_as_float(w.y));
-    return __float_as_uint(fmaxf(fmaxf(a, __uint_as_float(w.z)), __uint_as_float(w.w)));
+  __device__ void drop(uint32_t keep) {
+    drop4(a, keep);
+    drop4(b, keep >> 4);
+  }
+  __device__ uint32_t max(uint32_t m) const {          // a NaN loses
+    float x = __uint_as_float(m);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x = fmaxf(x, __uint_as_float(w[i]));
+    return __float_as_uint(x);
   }
   __device__ static float value(uint32_t m) { return __uint_as_float(m); }
-  __device__ static void unpack(const uint4& w, float (&z)[4]) {
-    z[0] = __uint_as_float(w.x); z[1] = __uint_as_float(w.y);
-    z[2] = __uint_as_float(w.z); z[3] = __uint_as_float(w.w);
+  __device__ void unpack(float (&z)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(w[i]);
   }
 };
 // Pairs of 16-bit values
 template <typename T, typename T2, uint32_t kPairNone>
-struct Packed16 {
+struct Octet16 {
+  uint4 a;
   static constexpr uint32_t kNone = kPairNone;
-  __device__ static void drop(uint4& w, uint32_t keep) {
+  __device__ void load(const T* z) { a = *reinterpret_cast<const uint4*>(z); }
+  __device__ void drop(uint32_t keep) {
     const uint32_t s = spread4(keep), t = spread4(keep >> 4);
-    w.x = keep_or(w.x, signs<0x9988>(s), kNone);
-    w.y = keep_or(w.y, signs<0xbbaa>(s), kNone);
-    w.z = keep_or(w.z, signs<0x9988>(t), kNone);
-    w.w = keep_or(w.w, signs<0xbbaa>(t), kNone);
+    a.x = keep_or(a.x, signs<0x9988>(s), kNone);
+    a.y = keep_or(a.y, signs<0xbbaa>(s), kNone);
+    a.z = keep_or(a.z, signs<0x9988>(t), kNone);
+    a.w = keep_or(a.w, signs<0xbbaa>(t), kNone);
   }
-  __device__ static uint32_t none() { return kNone; }
   __device__ static T2 pair(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
-  __device__ static uint32_t max(uint32_t m, const uint4& w) {       // a NaN loses
-    const T2 a = __hmax2(__hmax2(pair(m), pair(w.x)), pair(w.y));
-    const T2 b = __hmax2(__hmax2(a, pair(w.z)), pair(w.w));
-    return *reinterpret_cast<const uint32_t*>(&b);
+  __device__ uint32_t max(uint32_t m) const {          // a NaN loses
+    const T2 x = __hmax2(__hmax2(pair(m), pair(a.x)), pair(a.y));
+    const T2 y = __hmax2(__hmax2(x, pair(a.z)), pair(a.w));
+    return *reinterpret_cast<const uint32_t*>(&y);
   }
   __device__ static float value(uint32_t m) {
     const T2 p = pair(m);
     return fmaxf(widen(p.x), widen(p.y));
   }
-  __device__ static void unpack(const uint4& w, float (&z)[8]) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+  __device__ void unpack(float (&z)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      z[2 * i] = widen(pair(a[i]).x);
-      z[2 * i + 1] = widen(pair(a[i]).y);
+      z[2 * i] = widen(pair(w[i]).x);
+      z[2 * i + 1] = widen(pair(w[i]).y);
     }
   }
 };
 template <>
-struct Packed<__nv_bfloat16> : Packed16<__nv_bfloat16, __nv_bfloat162, 0xff80ff80u> {};
+struct Octet<__nv_bfloat16> : Octet16<__nv_bfloat16, __nv_bfloat162, 0xff80ff80u> {};
 template <>
-struct Packed<__half> : Packed16<__half, __half2, 0xfc00fc00u> {};
+struct Octet<__half> : Octet16<__half, __half2, 0xfc00fc00u> {};
 
 // Unsigned order of the keys is the order of the floats; +0 and -0 are one
 // value. Not for NaN.
 __device__ inline uint32_t ordered(float z) {
   const uint32_t u = __float_as_uint(z + 0.f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-__device__ inline unsigned long long choice_key(float z, int v) {
-  return ((unsigned long long)ordered(z) << 32) | (uint32_t)~v;
 }
 
 // The rows of sequence b, or none (T = 0) where its offsets are not usable.
@@ -187,10 +205,6 @@ __device__ inline int rows_of(const TargetParams& p, int b, int* first, bool tel
   return hi - lo;
 }
 
-// 32 bits of a bitmap from bit `o` on.
-__device__ inline uint32_t bits_at(const uint32_t* map, int o) {
-  return __funnelshift_r(map[o >> 5], map[(o >> 5) + 1], o & 31);
-}
 
 // The row's mask, or kNoMask / kShut (an index past the masks there are: closed
 // rather than open).
@@ -207,300 +221,408 @@ __device__ inline const uint32_t* mask_words(const TargetParams& p, int m) {
   return reinterpret_cast<const uint32_t*>(p.mask) + (size_t)m * p.mask_stride;
 }
 
-template <typename T, int NV>
-struct Window {
-  static constexpr int kVec = 16 / sizeof(T);
-  static constexpr int kTokens = kThreads * kVec * NV;
-  // The bitmap begins 32 tokens before the window: a shifted row's window
-  // begins up to kVec - 1 tokens early.
+// Parameters of sequence b
+struct SeqParams {
+  int first, T;                      // its rows
+  float r, pres, freq;
+  bool penal;
+  int bias0, bias1;
+  const int16_t* state;
+
+  __device__ SeqParams(const TargetParams& p, int b, bool tell) {
+    const float rep = p.repetition ? p.repetition[b] : 1.f;
+    pres = p.presence ? p.presence[b] : 0.f;
+    freq = p.frequency ? p.frequency[b] : 0.f;
+    bias0 = p.bias_off ? p.bias_off[b] : 0;
+    bias1 = p.bias_off ? p.bias_off[b + 1] : 0;
+    T = rows_of(p, b, &first, tell);
+    r = rep > 0.f && rep < INFINITY ? rep : 1.f;
+    penal = p.state && (r != 1.f || pres != 0.f || freq != 0.f);
+    state = p.state + (size_t)b * p.state_stride;
+    if (bias0 < 0 || bias1 < bias0 || bias1 > p.num_bias) {
+      if (tell) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
+      bias0 = bias1 = 0;
+    }
+  }
+  __device__ bool special() const { return penal || bias1 > bias0; }
+};
+
+// A bit for each of 8 state entries that is not zero
+__device__ inline uint32_t touched(const uint4& w) {
+  // bit 15 of a half that is not zero: the carry out of its lower 15 bits, or the
+  // bit itself; then the eight bits side by side
+  auto halves = [](uint32_t a) { return (((a & 0x7fff7fffu) + 0x7fff7fffu) | a) & 0x80008000u; };
+  const uint32_t m = (halves(w.x) >> 15) | (halves(w.y) >> 13) | (halves(w.z) >> 11) | (halves(w.w) >> 9);
+  return (m | (m >> 15)) & 0xffu;
+}
+
+template <typename T>
+struct Segment {
+  static constexpr int kTokens = 1024;
+  static constexpr int kOctets = 8 / sizeof(T);  // a lane's of a row in flight: 64 bytes
+  static constexpr int kBlock = 32 * 8 * kOctets;        // tokens of a row in flight
+  static constexpr int kBlocks = kTokens / kBlock;
+  static constexpr int kEarly = 16 / sizeof(T) - 1;
+  // The bitmap begins 32 tokens before the segment: a shifted row's segment
+  // begins up to kEarly tokens early.
   static constexpr int kBits = kTokens + 32;
   static constexpr int kWords = kBits / 32;
 };
 
-// One row's vectors of a thread: the logits and, where a mask applies, its bits.
-template <typename T, int NV>
+// A lane's octets of a row: the logits, and the words of the row's mask that hold
+// their bits (all ones without a mask). Octet n starts 256 tokens, 8 words, after
+// the one before it, so a bit's place in its word is the same for all n. kAligned:
+// every row begins on 16 bytes, and an octet's bits never cross a word.
+template <typename T, bool kAligned>
 struct RowVecs {
-  static constexpr int kVec = 16 / sizeof(T);
-  uint4 raw[NV];
-  uint32_t bits[NV];
+  static constexpr int N = Segment<T>::kOctets;
+  Octet<T> raw[N];
+  uint32_t w0[N], w1[N];
 
-  // v0: the thread's first token; vector n starts 32 * kVec * n after it.
-  __device__ void load(const T* z_row, const uint32_t* mask, int v0, int V) {
+  // z, q: where octet 0 and the mask word of its first token v0 are; q == nullptr:
+  // no mask. Every octet lies inside the row.
+  __device__ void load(const T* z, const uint32_t* q, int v0) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int v = v0 + n * 32 * kVec;
-      bits[n] = kAll;
-      if (v >= 0 && v + kVec <= V) {
-        raw[n] = *reinterpret_cast<const uint4*>(z_row + v);
-        if (mask) {
-          bits[n] = mask[v >> 5] >> (v & 31);
-          if ((v & 31) > 32 - kVec) bits[n] |= mask[(v >> 5) + 1] << (32 - (v & 31));
-        }
-      } else {                       // across an end of the row, or past it
-        T part[kVec];
-        uint32_t on = 0;
+    for (int n = 0; n < N; ++n) raw[n].load(z + n * 256);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const bool in = v + i >= 0 && v + i < V;
-          part[i] = in ? z_row[v + i] : T{};
-          if (in && (!mask || (mask[(v + i) >> 5] >> ((v + i) & 31)) & 1)) on |= 1u << i;
-        }
-        memcpy(&raw[n], part, 16);
-        bits[n] = on;
+    for (int n = 0; n < N; ++n) w0[n] = w1[n] = kAll;
+    if (q) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        w0[n] = q[n * 8];
+        if (!kAligned && (v0 & 31) > 24) w1[n] = q[n * 8 + 1];
       }
     }
+  }
+  // The same where octets may cross an end of the row or lie past it. z_row, mask:
+  // of the row; g0: v0 of lane 0. One octet crosses each end at most: its values
+  // come one a lane, by way of shared memory.
+  __device__ void load_end(const T* z_row, const uint32_t* mask, int g0, int V, Octet<T>* stage,
+                           int lane) {
+    const int high = g0 + ((V - g0) & ~7);       // the octet that the row's end is in
+    const int e = lane < 8 ? g0 + lane : high + lane - 8;
+    T one{};
+    if (lane < 16 && e >= 0 && e < V) one = z_row[e];
+    const int words = (V + 31) >> 5;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int v = g0 + lane * 8 + n * 256, sh = v & 31, w = v >> 5;
+      const int from = v < 0 ? -v : 0, to = V - v < 8 ? V - v : 8;
+      if (v >= 0 && v + 8 <= V) raw[n].load(z_row + v);
+      uint32_t on = to > 0 && from < 8 ? ((1u << to) - 1) & ~((1u << from) - 1) : 0;
+      if (mask && on)
+        on &= __funnelshift_r(w >= 0 && w < words ? mask[w] : 0u,
+                              w + 1 >= 0 && w + 1 < words ? mask[w + 1] : 0u, sh);
+      w0[n] = on << sh;
+      w1[n] = sh ? on >> (32 - sh) : 0;
+    }
+    __syncwarp();
+    if (lane < 16) reinterpret_cast<T*>(stage)[lane] = one;
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int v = g0 + lane * 8 + n * 256;
+      if (v < 0 || v + 8 > V) raw[n] = stage[v == high ? 1 : 0];
+    }
+  }
+  // The mask bits of octet n (upper bits: others')
+  __device__ uint32_t bits(int n, int v0) const {
+    return kAligned ? w0[n] >> (v0 & 31) : __funnelshift_r(w0[n], w1[n], v0 & 31);
   }
 };
 
-template <typename T, int NV, bool kOut>
-__global__ void __launch_bounds__(kThreads) choose_kernel(TargetParams p) {
-  using W = Window<T, NV>;
-  using P = Packed<T>;
-  constexpr int kVec = W::kVec;
-  constexpr int kRows = 4 / NV;      // rows whose loads are in flight together
-  __shared__ uint32_t s_special[W::kWords + 1], s_block[W::kWords + 1];
-  __shared__ uint16_t s_list[W::kBits];
-  __shared__ int s_count;
-  __shared__ int s_tok[kMaxBlock], s_mask[kChunk];
-  // best dense value (key of the warp that holds it), best special token
-  __shared__ unsigned long long s_dense[kChunk], s_best[kChunk];
-  extern __shared__ int s_bias[];    // [kBits] last bias entry + 1 of a token; with biases only
+// Shared memory of a warp. Where there are biases, int [kBits] for each warp
+// follows all of them: a token's last bias entry + 1.
+template <typename T>
+struct WarpSmem {
+  uint32_t map[Segment<T>::kWords + 1];    // special tokens
+  uint32_t block[Segment<T>::kWords + 1];  // those of the block among them
+  uint16_t list[Segment<T>::kBits];
+  // the octets across a row's ends; a lane's octets that have a maximum
+  alignas(16) Octet<T> stage[Segment<T>::kOctets > 2 ? Segment<T>::kOctets : 2];
+};
 
+template <typename T, bool kOut, bool kAligned>
+__global__ void __launch_bounds__(32 * kWarpsPerCta, 16 / kWarpsPerCta)
+choose_kernel(TargetParams p) {
+  using S = Segment<T>;
+  using Vecs = RowVecs<T, kAligned>;
+  constexpr int N = S::kOctets;
+  constexpr int kGroups = S::kTokens / 8 / 32;   // state groups of 8 entries a lane
+  constexpr int kIds = 10;
+  extern __shared__ __align__(16) unsigned char smem[];
   allow_dependent_launch();
-  const int win = blockIdx.x % p.windows, unit = blockIdx.x / p.windows;
-  const int b = unit / p.chunks, skip = unit % p.chunks * kChunk;    // rows before this chunk
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int block_first;
-  const int T_seq = rows_of(p, b, &block_first, win == 0 && skip == 0 && tid == 0);
-  if (T_seq <= skip) return;
-  const int T_b = min(T_seq - skip, kChunk), first = block_first + skip;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  WarpSmem<T>& sm = reinterpret_cast<WarpSmem<T>*>(smem)[warp];
+  int* s_bias = reinterpret_cast<int*>(smem + kWarpsPerCta * sizeof(WarpSmem<T>)) + warp * S::kBits;
+
+  const unsigned work = blockIdx.x * kWarpsPerCta + warp;
+  const int run = work % p.runs;
+  const unsigned unit = work / p.runs;
+  const int chunk = unit % p.chunks, b = unit / p.chunks;
+  if (b >= p.num_seqs) return;
+  const int skip = chunk * kChunk;               // rows before this chunk
+  const bool lead = chunk == 0 && run == 0 && lane == 0;
+  const SeqParams q(p, b, lead);
+  const int T_b = min(q.T - skip, kChunk), first = q.first + skip;
+  if (T_b <= 0) return;
   const int V = p.vocab;
-  const int lo = win * W::kTokens, base = lo - 32;          // first token of bitmap bit 0
-  const int wlo = max(0, lo - (kVec - 1)), whi = min(V, lo + W::kTokens);
-  const T* logits = static_cast<const T*>(p.logits);
-  // First token of this thread's vectors in a row: a warp has 32 * NV vectors in
-  // a stretch, so that warps follow the order of the tokens.
-  auto shift_of = [&](const T* z_row) {
-    return (int)((reinterpret_cast<uintptr_t>(z_row) & 15) / sizeof(T));
-  };
-  auto first_of = [&](int w, int shift) { return lo + (w * NV * 32 + lane) * kVec - shift; };
-  RowVecs<T, NV> x[kRows];
-  // Rows t0 .. of the chunk; mask(t) tells a row's mask.
-  auto load_rows = [&](int t0, auto mask) {
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (t0 + u >= T_b) break;
-      const T* z_row = logits + (first + t0 + u) * p.stride;
-      const int m = mask(t0 + u);
-      x[u].load(z_row, m >= 0 ? mask_words(p, m) : nullptr, first_of(warp, shift_of(z_row)), V);
-    }
-  };
-  load_rows(0, [&](int t) { return mask_of(p, first + t); });
+  const bool biased = q.bias1 > q.bias0, special = q.special();
+  const T* z_first = static_cast<const T*>(p.logits) + first * p.stride;
+  const int seg0 = run * p.span, seg1 = min(seg0 + p.span, p.segments);
 
-  // --- what is special in this window --------------------------------------
-  const float rep = p.repetition ? p.repetition[b] : 1.f;
-  const float r = rep > 0.f && rep < INFINITY ? rep : 1.f;
-  const float pres = p.presence ? p.presence[b] : 0.f;
-  const float freq = p.frequency ? p.frequency[b] : 0.f;
-  const bool penal = p.state && (r != 1.f || pres != 0.f || freq != 0.f);
-  int bias0 = 0, bias1 = 0;
-  if (p.bias_off) {
-    bias0 = p.bias_off[b];
-    bias1 = p.bias_off[b + 1];
-    if (bias0 < 0 || bias1 < bias0 || bias1 > p.num_bias) {
-      if (win == 0 && skip == 0 && tid == 0) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
-      bias0 = bias1 = 0;
+  // lane t: the mask words of row t, and its best choice so far
+  const int my_mask = lane < T_b ? mask_of(p, first + lane) : kNoMask;
+  const unsigned long long my_words = my_mask >= 0 ? (unsigned long long)mask_words(p, my_mask) : 0;
+  unsigned long long best = 0;
+  auto words_of = [&](int t) {
+    return p.mask ? reinterpret_cast<const uint32_t*>(__shfl_sync(kAll, my_words, t)) : nullptr;
+  };
+  const unsigned shut = __ballot_sync(kAll, my_mask == kShut);
+  auto shift_of = [&](int t) {
+    return kAligned ? 0
+                    : (int)((reinterpret_cast<uintptr_t>(z_first + t * p.stride) & 15) / sizeof(T));
+  };
+  // First token of this lane's octets in row t of a block (kBlocks to a segment)
+  auto first_of = [&](int block, int t) { return block * S::kBlock + lane * 8 - shift_of(t); };
+  Vecs x;                                        // the row whose loads are in flight
+  auto load_row = [&](int block, int t) {
+    const int v0 = first_of(block, t);
+    const T* z_row = z_first + t * p.stride;
+    const uint32_t* mask = words_of(t);
+    if ((kAligned || block > 0) && (block + 1) * S::kBlock <= V)
+      x.load(z_row + v0, mask ? mask + (v0 >> 5) : nullptr, v0);
+    else
+      x.load_end(z_row, mask, v0 - lane * 8, V, sm.stage, lane);
+  };
+  uint4 st[kGroups];
+  auto load_state = [&](int seg) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int v = seg * S::kTokens + (i * 32 + lane) * 8;
+      st[i] = v < V ? *reinterpret_cast<const uint4*>(q.state + v) : make_uint4(0, 0, 0, 0);
     }
-  }
-  const bool biased = bias1 > bias0, special = penal || biased;
-  for (int i = tid; i <= W::kWords; i += kThreads) s_special[i] = s_block[i] = 0;
+  };
+  if (q.penal) load_state(seg0);
+  load_row(seg0 * S::kBlocks, 0);
   if (biased)
-    for (int i = tid; i < W::kBits; i += kThreads) s_bias[i] = 0;
-  for (int t = tid; t < skip + T_b; t += kThreads) s_tok[t] = penal ? p.tokens[block_first + t] : -1;
-  if (tid < T_b) {
-    s_dense[tid] = s_best[tid] = 0;
-    s_mask[tid] = mask_of(p, first + tid);
-  }
-  if (tid == 0) s_count = 0;
-  __syncthreads();
-  if (special) {
-    if (penal) {
-      const int16_t* st = p.state + (size_t)b * p.state_stride;
-      for (int v = (wlo & ~7) + tid * 8; v < whi; v += kThreads * 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(st + v);
-        if (!(w.x | w.y | w.z | w.w)) continue;
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-        uint32_t hit = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          hit |= ((a[i] & 0xffffu) ? 1u << (2 * i) : 0u) | ((a[i] >> 16) ? 2u << (2 * i) : 0u);
-        if (v + 8 > V) hit &= (1u << (V - v)) - 1;           // the row's padding
-        const int o = v - base;
-        atomicOr(&s_special[o >> 5], hit << (o & 31));      // v is a multiple of 8
-      }
-      for (int t = tid; t < skip + T_b; t += kThreads) {
-        const int v = s_tok[t];
-        if (v >= wlo && v < whi) {
-          const int o = v - base;
-          atomicOr(&s_special[o >> 5], 1u << (o & 31));
-          atomicOr(&s_block[o >> 5], 1u << (o & 31));
-        }
-      }
-    }
-    for (int e = bias0 + tid; e < bias1; e += kThreads) {
-      const int v = p.bias_ids[e];
-      if (v >= wlo && v < whi) {
-        const int o = v - base;
-        atomicOr(&s_special[o >> 5], 1u << (o & 31));
-        atomicMax(&s_bias[o], e - bias0 + 1);
-      }
-    }
-    __syncthreads();
-    for (int w = tid; w < W::kWords; w += kThreads) {
-      uint32_t m = s_special[w];
-      if (!m) continue;
-      int at = atomicAdd(&s_count, __popc(m));
-      for (; m; m &= m - 1) s_list[at++] = (uint16_t)(w * 32 + __ffs(m) - 1);
-    }
-    __syncthreads();
-  }
+    for (int i = lane; i < S::kBits; i += 32) s_bias[i] = 0;
 
-  auto mask_at = [&](int t) {
-    const int m = s_mask[t];
-    return m >= 0 ? mask_words(p, m) : nullptr;
-  };
-  // The allowed values of vector n that are not special; the others -inf.
-  auto keep_bits = [&](const RowVecs<T, NV>& x, int n, int v0, bool shut) -> uint32_t {
-    if (shut) return 0;
-    return special ? x.bits[n] & ~bits_at(s_special, v0 + n * 32 * kVec - base) : x.bits[n];
-  };
-
-  // --- dense pass: the largest value of every token that is not special -----
-  for (int t0 = 0; t0 < T_b; t0 += kRows) {
-    RowVecs<T, NV> now[kRows];
+  for (int seg = seg0; seg < seg1; ++seg) {
+    const int lo = seg * S::kTokens, base = lo - 32;        // first token of bitmap bit 0
+    const int wlo = max(0, lo - S::kEarly), whi = min(V, lo + S::kTokens);
+    int listed = 0;
+    auto special_bits = [&](int n, int v0) -> uint32_t {
+      const uint32_t* w = sm.map + ((v0 - base) >> 5) + n * 8;
+      return kAligned ? w[0] >> (v0 & 31) : __funnelshift_r(w[0], w[1], v0 & 31);
+    };
+    if (special) {
+      // --- mark and list the special tokens -----------------------------------
+      for (int i = lane; i <= S::kWords; i += 32) sm.block[i] = 0;
+      if (lane == 0) {
+        // the 8 tokens before the segment, of which a shifted row may have some
+        sm.map[0] = !kAligned && q.penal && lo > 0
+                        ? touched(*reinterpret_cast<const uint4*>(q.state + lo - 8)) << 24 : 0;
+        sm.map[S::kWords] = 0;
+      }
+      uint8_t* bytes = reinterpret_cast<uint8_t*>(sm.map + 1);
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) now[u] = x[u];
-    load_rows(t0 + kRows, [&](int t) { return s_mask[t]; });
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int t = t0 + u;
-      if (t >= T_b) break;
-      const int v0 = first_of(warp, shift_of(logits + (first + t) * p.stride));
-      const bool shut = s_mask[t] == kShut;
-      uint32_t m = P::none();
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const uint32_t keep = keep_bits(now[u], n, v0, shut);
-        if constexpr (kOut) {
-          // special tokens keep their logit: in place, the next pass reads it
-          const int v = v0 + n * 32 * kVec;
-          const uint32_t open = shut ? 0 : now[u].bits[n];
-          const uint32_t sp = special ? bits_at(s_special, v - base) : 0;
-          float* o = p.out + (first + t) * p.out_stride + v;
-          float y[kVec];
-          P::unpack(now[u].raw[n], y);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) y[i] = ((open | sp) >> i) & 1 ? y[i] : -INFINITY;
-          if (v >= 0 && v + kVec <= V && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < kVec; i += 4)
-              *reinterpret_cast<float4*>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-              if (v + i >= 0 && v + i < V) o[i] = y[i];
+      for (int i = 0; i < kGroups; ++i) {
+        const int g = i * 32 + lane, v = lo + 8 * g;
+        uint32_t hit = q.penal ? touched(st[i]) : 0;
+        if (lo + S::kTokens > V && v + 8 > V)          // the row's padding
+          hit &= v < V ? (1u << (V - v)) - 1 : 0;
+        bytes[g] = (uint8_t)hit;
+      }
+      __syncwarp();
+      if (q.penal)
+        for (int t = lane; t < skip + T_b; t += 32) {
+          const int v = p.tokens[q.first + t];
+          if (v >= wlo && v < whi) {
+            atomicOr(&sm.map[(v - base) >> 5], 1u << ((v - base) & 31));
+            atomicOr(&sm.block[(v - base) >> 5], 1u << ((v - base) & 31));
           }
         }
-        P::drop(now[u].raw[n], keep);
-        m = P::max(m, now[u].raw[n]);
+      for (int e0 = q.bias0 + lane; e0 < q.bias1; e0 += 32 * kIds) {
+        int id[kIds];                            // the loads of all before the first use
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) id[i] = e0 + 32 * i < q.bias1 ? p.bias_ids[e0 + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < kIds; ++i)
+          if (id[i] >= wlo && id[i] < whi) {
+            atomicOr(&sm.map[(id[i] - base) >> 5], 1u << ((id[i] - base) & 31));
+            atomicMax(&s_bias[id[i] - base], e0 + 32 * i - q.bias0 + 1);
+          }
       }
-      const uint32_t top = __reduce_max_sync(kAll, ordered(P::value(m)));
-      if (lane == 0 && top > ordered(-INFINITY))
-        atomicMax(&s_dense[t], ((unsigned long long)top << 32) | (uint32_t)~warp);
+      __syncwarp();
+      // a word a lane; the one before the segment goes to lane 0 as well
+      static_assert(S::kWords <= 33, "words of a bitmap");
+      uint32_t m = lane + 1 < S::kWords ? sm.map[lane + 1] : 0;
+      const uint32_t before = !kAligned && lane == 0 ? sm.map[0] : 0;
+      const int mine = __popc(m) + __popc(before);
+      int at = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(kAll, at, o);
+        if (lane >= o) at += n;
+      }
+      listed = __shfl_sync(kAll, at, 31);
+      at -= mine;
+      for (uint32_t w = before; w; w &= w - 1) sm.list[at++] = (uint16_t)(__ffs(w) - 1);
+      for (; m; m &= m - 1) sm.list[at++] = (uint16_t)(lane * 32 + 31 + __ffs(m));
+      __syncwarp();
     }
-  }
-  __syncthreads();
 
-  // --- where the dense best is: its first place in that warp's stretch ------
-  for (int t = warp; t < T_b; t += kWarps) {
-    const unsigned long long d = s_dense[t];
-    if (d == 0) continue;
-    const T* z_row = logits + (first + t) * p.stride;
-    const int v0 = first_of((int)~(uint32_t)d, shift_of(z_row));
-    RowVecs<T, NV> y;
-    y.load(z_row, mask_at(t), v0, V);
-    uint32_t at = UINT_MAX;
+    // --- a lane's first special token: its loads run under the dense pass ------
+    // Token list[e]: what its processing for rows 0 .. T_b - 1 reads.
+    struct {
+      int o, v, held, entry;
+      float bias;
+      T z[kChunk];
+      uint32_t word[kChunk];
+    } sp;
+    auto load_special = [&](int e) {
+      const bool live = e < listed;
+      sp.o = live ? sm.list[e] : 32;
+      sp.v = base + sp.o;
+      sp.held = q.penal && live ? q.state[sp.v] : 0;
+      sp.entry = biased && live ? s_bias[sp.o] : 0;
+      sp.bias = sp.entry ? p.bias_values[q.bias0 + sp.entry - 1] : 0.f;
+      const T* zp = z_first + sp.v;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      P::drop(y.raw[n], keep_bits(y, n, v0, false));
-      float z[kVec];
-      P::unpack(y.raw[n], z);
-#pragma unroll
-      for (int i = kVec - 1; i >= 0; --i)
-        if (ordered(z[i]) == (uint32_t)(d >> 32)) at = min(at, (uint32_t)(v0 + n * 32 * kVec + i));
-    }
-    at = __reduce_min_sync(kAll, at);
-    if (lane == 0) atomicMax(&s_best[t], (d & 0xffffffff00000000ull) | (uint32_t)~at);
-  }
-
-  // --- the special tokens: a lane takes one for kRowBatch rows --------------
-  const int listed = s_count, groups = (T_b + kRowBatch - 1) / kRowBatch;
-  const int chunks = (listed + 31) / 32;
-  for (int i = warp; i < chunks * groups; i += kWarps) {
-    const int e = (i / groups) * 32 + lane;
-    if (e >= listed) continue;
-    const int o = s_list[e], v = base + o;
-    const int t0 = i % groups * kRowBatch, t1 = min(t0 + kRowBatch, T_b);
-    float z[kRowBatch];
-    uint32_t word[kRowBatch];
-#pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) {
-      if (t0 + u >= t1) continue;
-      z[u] = widen(logits[(first + t0 + u) * p.stride + v]);
-      const uint32_t* mask = mask_at(t0 + u);
-      word[u] = mask ? mask[v >> 5] : (s_mask[t0 + u] == kShut ? 0 : kAll);
-    }
-    int count = 0;
-    bool in_prompt = false;
-    if (penal) {
-      const int st = p.state[(size_t)b * p.state_stride + v];
-      in_prompt = st < 0;
-      count = st & 0x7fff;
-    }
-    const bool in_block = (s_block[o >> 5] >> (o & 31)) & 1;
-    if (in_block)
-      for (int s = 0; s < skip + t0; ++s) count += s_tok[s] == v;
-    const int entry = biased ? s_bias[o] : 0;
-    const float bias = entry ? p.bias_values[bias0 + entry - 1] : 0.f;
-#pragma unroll
-    for (int u = 0; u < kRowBatch; ++u) {
-      const int t = t0 + u;
-      if (t >= t1) break;
-      if (in_block) count += s_tok[skip + t] == v;
-      const int row = first + t;
-      // the row's own window is shifted with it
-      const int from = lo - shift_of(logits + row * p.stride);
-      if (v < from || v >= from + W::kTokens) continue;
-      float y = z[u];
-      if (penal) {
-        if (count > 0 || in_prompt) y = y > 0.f ? __fdiv_rn(y, r) : __fmul_rn(y, r);
-        y = __fsub_rn(y, __fmul_rn(freq, (float)count));
-        if (count > 0) y = __fsub_rn(y, pres);
+      for (int t = 0; t < kChunk; ++t) {
+        if (t >= T_b) break;
+        const uint32_t* mask = words_of(t);
+        // the row's own segment is shifted with it
+        const int from = lo - shift_of(t);
+        sp.z[t] = T{};
+        sp.word[t] = 0;
+        if (live && (kAligned || (sp.v >= from && sp.v < from + S::kTokens))) {
+          sp.z[t] = *zp;
+          sp.word[t] = mask ? mask[sp.v >> 5] : kAll;
+        }
+        zp += p.stride;
       }
-      if (entry) y = __fadd_rn(y, bias);
-      if (!((word[u] >> (v & 31)) & 1)) y = -INFINITY;
-      if constexpr (kOut) p.out[row * p.out_stride + v] = y;
-      if (y > -INFINITY) {           // not for NaN
-        const unsigned long long k = choice_key(y, v);
-        if (k > s_best[t]) atomicMax(&s_best[t], k);
+    };
+    // --- dense: the largest value of every other token -------------------------
+    auto take_row = [&](Vecs& x, int block, int t) {
+      const int v0 = first_of(block, t);
+      const bool closed = (shut >> t) & 1;
+      uint32_t m = Octet<T>::kNone;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const uint32_t open = closed ? 0 : x.bits(n, v0);
+        const uint32_t spec = special ? special_bits(n, v0) : 0;
+        if constexpr (kOut) {
+          // special tokens keep their logit: in place, more than 32 are read again
+          const int v = v0 + n * 256;
+          float* o = p.out + (first + t) * p.out_stride + v;
+          float z[8];
+          x.raw[n].unpack(z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = ((open | spec) >> i) & 1 ? z[i] : -INFINITY;
+          if (v >= 0 && v <= V - 8 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            *reinterpret_cast<float4*>(o) = make_float4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(z[4], z[5], z[6], z[7]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (v + i >= 0 && v + i < V) o[i] = z[i];
+          }
+        }
+        x.raw[n].drop(open & ~spec);
+        m = x.raw[n].max(m);
+      }
+      const uint32_t key = ordered(Octet<T>::value(m)), top = __reduce_max_sync(kAll, key);
+      // an equal value of an earlier segment has the lower index
+      const uint32_t held = __shfl_sync(kAll, (uint32_t)(best >> 32), t);
+      if (top <= ordered(-INFINITY) || top <= held) return;
+      // its place: every lane that has it shows its values to the warp
+      uint32_t at = UINT_MAX;
+      for (uint32_t has = __ballot_sync(kAll, key == top); has; has &= has - 1) {
+        const int who = __ffs(has) - 1;
+        __syncwarp();
+        if (lane == who) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) sm.stage[n] = x.raw[n];
+        }
+        __syncwarp();
+        const bool in = lane < N * 8;
+        const float z = in ? widen(reinterpret_cast<const T*>(sm.stage)[lane]) : -INFINITY;
+        const int i = __ffs(__ballot_sync(kAll, in && ordered(z) == top)) - 1;
+        at = min(at, (uint32_t)(v0 + (who - lane) * 8 + i / 8 * 256 + i % 8));
+      }
+      if (lane == t) best = ((unsigned long long)top << 32) | (uint32_t)~at;
+    };
+    for (int e0 = 0; e0 == 0 || e0 < listed; e0 += 32) {
+      if (special) load_special(e0 + lane);
+      if (e0 == 0) {
+        const int block1 = (seg + 1) * S::kBlocks;
+        for (int block = seg * S::kBlocks; block < block1; ++block) {
+          for (int t = 0; t < T_b; ++t) {
+            Vecs now = x;
+            const bool more = t + 1 < T_b;       // or else the next block's first row
+            if (more || block + 1 < seg1 * S::kBlocks) load_row(more ? block : block + 1, more ? t + 1 : 0);
+            if (!more && block + 1 == block1 && q.penal && seg + 1 < seg1) load_state(seg + 1);
+            take_row(now, block, t);
+          }
+        }
+        if constexpr (kOut) __syncwarp();        // the special ones' places are written
+      }
+      if (!special) break;
+      // --- the special tokens ----------------------------------------------------
+      const bool live = e0 + lane < listed, in_prompt = sp.held < 0;
+      const bool in_block = live && (sm.block[sp.o >> 5] >> (sp.o & 31)) & 1;
+      int count = sp.held & 0x7fff;
+      if (in_block)
+        for (int s = 0; s < skip; ++s) count += p.tokens[q.first + s] == sp.v;
+      uint32_t key[kChunk];
+#pragma unroll
+      for (int t = 0; t < kChunk; ++t) {
+        key[t] = 0;
+        if (t >= T_b) break;
+        if (in_block) count += p.tokens[first + t] == sp.v;
+        float w = widen(sp.z[t]);
+        if (q.penal) {
+          if (count > 0 || in_prompt) w = w > 0.f ? __fdiv_rn(w, q.r) : __fmul_rn(w, q.r);
+          w = __fsub_rn(w, __fmul_rn(q.freq, (float)count));
+          if (count > 0) w = __fsub_rn(w, q.pres);
+        }
+        if (sp.entry) w = __fadd_rn(w, sp.bias);
+        if (!((sp.word[t] >> (sp.v & 31)) & 1) || (shut >> t) & 1) w = -INFINITY;
+        if constexpr (kOut) {
+          const int from = lo - shift_of(t);
+          if (live && (kAligned || (sp.v >= from && sp.v < from + S::kTokens)))
+            p.out[(first + t) * p.out_stride + sp.v] = w;
+        }
+        if (w > -INFINITY) key[t] = ordered(w);  // a NaN is no candidate
+      }
+      // the warp's best of each row, to the lane that keeps it; no branch between,
+      // so that the rows' reductions overlap
+      uint32_t top = 0, at = 0;
+#pragma unroll
+      for (int t = 0; t < kChunk; ++t) {
+        if (t >= T_b) break;
+        const uint32_t m = __reduce_max_sync(kAll, key[t]);
+        const uint32_t v = __reduce_min_sync(kAll, key[t] == m ? (uint32_t)sp.v : UINT_MAX);
+        if (lane == t) {
+          top = m;
+          at = v;
+        }
+      }
+      if (top > 0) {
+        const unsigned long long c = ((unsigned long long)top << 32) | (uint32_t)~at;
+        if (c > best) best = c;
       }
     }
+    if (biased)                                  // clean for the next segment
+      for (int e = lane; e < listed; e += 32) s_bias[sm.list[e]] = 0;
+    __syncwarp();
   }
-  __syncthreads();
-  if (tid < T_b) p.part[(size_t)(first + tid) * p.windows + win] = s_best[tid];
+  if (lane < T_b) p.part[(size_t)(first + lane) * p.runs + run] = best;
 }
 
-// One CTA a sequence, one warp a row: the largest key over the windows.
+// One CTA a sequence, one warp a row: the largest key over the row's runs.
 constexpr int kMergeThreads = 128;
 __global__ void __launch_bounds__(kMergeThreads) choose_merge_kernel(TargetParams p) {
   grid_dependency_wait();
@@ -508,9 +630,9 @@ __global__ void __launch_bounds__(kMergeThreads) choose_merge_kernel(TargetParam
   int first;
   const int T_b = rows_of(p, b, &first, false);
   for (int t = threadIdx.x >> 5; t < T_b; t += kMergeThreads / 32) {
-    const unsigned long long* part = p.part + (size_t)(first + t) * p.windows;
+    const unsigned long long* part = p.part + (size_t)(first + t) * p.runs;
     unsigned long long best = 0;
-    for (int w = lane; w < p.windows; w += 32) best = part[w] > best ? part[w] : best;
+    for (int w = lane; w < p.runs; w += 32) best = part[w] > best ? part[w] : best;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long y = __shfl_xor_sync(kAll, best, o);
@@ -520,36 +642,29 @@ __global__ void __launch_bounds__(kMergeThreads) choose_merge_kernel(TargetParam
   }
 }
 
-// Tokens of a window: one, two or four vectors a thread.
-int window_tokens(int dtype, int nv) { return kThreads * (dtype == SPLASH_F32 ? 4 : 8) * nv; }
-
-long long windows_for(int vocab, int dtype, int nv) {
-  // a shifted row's grid begins up to a vector early
-  const int w = window_tokens(dtype, nv), vec = dtype == SPLASH_F32 ? 4 : 8;
-  return ((long long)vocab + vec - 1 + w - 1) / w;
+long long segments_for(int vocab, int dtype, bool aligned) {
+  // a shifted row's grid begins early
+  const int early = aligned ? 0 : dtype == SPLASH_F32 ? Segment<float>::kEarly : Segment<__half>::kEarly;
+  constexpr int kTokens = Segment<float>::kTokens;
+  return ((long long)vocab + early + kTokens - 1) / kTokens;
 }
 
-template <typename T, int NV, bool kOut>
+template <typename T, bool kOut, bool kAligned>
 cudaError_t launch_choose(const TargetParams& p, cudaStream_t s) {
-  const int smem = p.bias_off ? (int)sizeof(int) * Window<T, NV>::kBits : 0;
-  if (smem > 0) {
-    const cudaError_t e = ensure_dynamic_smem<choose_kernel<T, NV, kOut>>(smem);
-    if (e != cudaSuccess) return e;
-  }
-  choose_kernel<T, NV, kOut>
-      <<<(unsigned)((long long)p.num_seqs * p.chunks * p.windows), kThreads, smem, s>>>(p);
+  const int smem = kWarpsPerCta * (int)(sizeof(WarpSmem<T>) +
+                                        (p.bias_off ? Segment<T>::kBits * sizeof(int) : 0));
+  const long long warps = (long long)p.num_seqs * p.chunks * p.runs;
+  choose_kernel<T, kOut, kAligned>
+      <<<(unsigned)((warps + kWarpsPerCta - 1) / kWarpsPerCta), 32 * kWarpsPerCta, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_choose_nv(const TargetParams& p, int nv, cudaStream_t s) {
-  if (p.out)
-    return nv == 1   ? launch_choose<T, 1, true>(p, s)
-           : nv == 2 ? launch_choose<T, 2, true>(p, s)
-                     : launch_choose<T, 4, true>(p, s);
-  return nv == 1   ? launch_choose<T, 1, false>(p, s)
-         : nv == 2 ? launch_choose<T, 2, false>(p, s)
-                   : launch_choose<T, 4, false>(p, s);
+cudaError_t launch_choose(const TargetParams& p, bool aligned, cudaStream_t s) {
+  static_assert(kWarpsPerCta * (sizeof(WarpSmem<T>) + Segment<T>::kBits * sizeof(int)) <= 48 * 1024,
+                "shared memory");
+  if (p.out) return aligned ? launch_choose<T, true, true>(p, s) : launch_choose<T, true, false>(p, s);
+  return aligned ? launch_choose<T, false, true>(p, s) : launch_choose<T, false, false>(p, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -665,8 +780,8 @@ int splash_token_state_stride(int vocab) {
 
 size_t splash_choose_targets_workspace_size(int num_rows, int vocab) {
   if (num_rows < 0 || vocab <= 0) return 0;
-  // the smallest windows any call makes
-  return sizeof(unsigned long long) * (size_t)num_rows * (size_t)windows_for(vocab, SPLASH_F32, 1);
+  // Runs are of 1024 tokens at least; shifted rows may have one more.
+  return sizeof(unsigned long long) * (size_t)num_rows * (size_t)(vocab / 1024 + 2);
 }
 
 int splash_choose_targets(const void* logits, int dtype, long long logits_stride, int num_rows,
@@ -706,27 +821,30 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
   const int sms = device_sm_count();
   if (sms <= 0) return SPLASH_ERR_CUDA;
 
-  // Up to four vectors a thread and row as long as that still fills the GPU: a
-  // window's set-up and merging are shared by more tokens. What the rows of a
-  // sequence make in chunks counts only as far as there are rows.
+  // A warp for each segment while that does not fill the GPU, then longer runs: a
+  // run's first loads and last merge are shared by more tokens. Chunks count only
+  // as far as there are rows.
+  const bool aligned = aligned16(logits) && logits_stride * es % 16 == 0;
   const int chunks = (max_block_len + kChunk - 1) / kChunk;
   const long long full = num_seqs + (long long)num_rows / kChunk;
   const long long units = num_seqs * (long long)chunks < full ? num_seqs * (long long)chunks : full;
-  int nv = 4;
-  while (nv > 1 && units * windows_for(vocab, dtype, nv) < 4LL * sms) nv /= 2;
-  const long long windows = windows_for(vocab, dtype, nv);
-  if (windows * num_seqs * chunks > INT_MAX) return SPLASH_ERR_UNSUPPORTED;
-  if (workspace_bytes < sizeof(unsigned long long) * (size_t)num_rows * (size_t)windows)
+  const long long segments = segments_for(vocab, dtype, aligned);
+  long long span = units * segments / (kWarpsPerSm * sms);
+  span = span < 1 ? 1 : span;
+  const long long runs = (segments + span - 1) / span;
+  if (runs * num_seqs > INT_MAX / (chunks + 1)) return SPLASH_ERR_UNSUPPORTED;
+  if (workspace_bytes < sizeof(unsigned long long) * (size_t)num_rows * (size_t)runs)
     return SPLASH_ERR_WORKSPACE_TOO_SMALL;
   TargetParams p{logits, logits_stride, num_rows, vocab, q_offsets, num_seqs, max_block_len,
                  block_tokens, penal ? state : nullptr, state_stride, repetition, presence,
                  frequency, num_bias > 0 ? bias_offsets : nullptr, bias_ids, bias_values, num_bias,
                  mask, mask_stride, mask_rows, num_masks, out, out_stride, target_tokens,
-                 static_cast<unsigned long long*>(workspace), (int)windows, chunks, device_status};
+                 static_cast<unsigned long long*>(workspace), (int)segments, (int)span, (int)runs,
+                 chunks, device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = dtype == SPLASH_F32    ? launch_choose_nv<float>(p, nv, s)
-                  : dtype == SPLASH_BF16 ? launch_choose_nv<__nv_bfloat16>(p, nv, s)
-                                         : launch_choose_nv<__half>(p, nv, s);
+  cudaError_t e = dtype == SPLASH_F32    ? launch_choose<float>(p, aligned, s)
+                  : dtype == SPLASH_BF16 ? launch_choose<__nv_bfloat16>(p, aligned, s)
+                                         : launch_choose<__half>(p, aligned, s);
   if (counted(e) != cudaSuccess) return SPLASH_ERR_CUDA;
   e = launch_dependent(choose_merge_kernel, dim3(num_seqs), dim3(kMergeThreads), 0, s, p);
   return counted(e) == cudaSuccess ? SPLASH_OK : SPLASH_ERR_CUDA;

@@ -135,4 +135,4 @@ def test_sizes(lib):
     assert [lib.splash_token_state_stride(v) for v in (0, -1, 1, 64, 65)] == [0, 0, 64, 64, 128]
     f = lib.splash_choose_targets_workspace_size
     assert f(-1, 10) == 0 and f(4, 0) == 0 and f(0, 10) == 0
-    assert f(4, 1000) == 8 * 4 and f(2, 1025) == 8 * 2 * 2
+    assert f(4, 1000) == 8 * 4 * 2 and f(2, 1025) == 8 * 2 * 3
