@@ -387,7 +387,7 @@ int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, 
                  aligned16(positions) && aligned16(slots), device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int fused = num_tokens <= kFusedTokens;
-  if (num_seqs <= kScanSmall && num_tokens <= 4 * kScanSmall * kTokensPerThread)
+  if (num_seqs <= kScanSmall && (!fused || num_tokens <= 4 * kScanSmall * kTokensPerThread))
     tables_scan_kernel<kScanSmall><<<1, kScanSmall, 0, s>>>(p, fused);
   else
     tables_scan_kernel<kScanLarge><<<1, kScanLarge, 0, s>>>(p, fused);

@@ -750,9 +750,17 @@ __global__ void __launch_bounds__(1024) history_reset_kernel(HistoryParams p, in
   int lo;
   const int end = counted_end(p, b, &lo, threadIdx.x == 0 && lo_v == 0);
   const int top = min(hi_v, p.vocab);
-  for (int i = lo + threadIdx.x; i < end; i += blockDim.x) {
-    const int v = p.tokens[i];
-    if (v >= lo_v && v < top) atomicAdd(&s_n[v - lo_v], 1);
+  constexpr int kAhead = 8;          // tokens whose loads are in flight
+  for (int i = lo + threadIdx.x; i < end; i += kAhead * blockDim.x) {
+    int v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const long long j = (long long)i + u * blockDim.x;
+      v[u] = j < end ? p.tokens[j] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (v[u] >= lo_v && v[u] < top) atomicAdd(&s_n[v[u] - lo_v], 1);
   }
   __syncthreads();
   uint32_t* row = reinterpret_cast<uint32_t*>(p.state + (size_t)b * p.stride);

@@ -363,14 +363,21 @@ def _check_all(specs, device_status) -> int:
     """specs: (tensor or None, name, dtype, ndim) of contiguous CUDA tensors, all
     on the current device. Returns the device index."""
     dev = torch.cuda.current_device()
-    for t, name, dtype, ndim in specs:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda \
-                or not t.is_contiguous() or t.dim() != ndim:
+    try:
+        for t, name, dtype, ndim in specs:
+            if t is not None and (t.dtype is not dtype or t.get_device() != dev
+                                  or t.dim() != ndim or not t.is_contiguous()):
+                break
+        else:
+            if device_status is None:
+                return dev
+    except AttributeError:
+        pass
+    for t, name, dtype, ndim in specs:           # the same with words
+        if t is not None:
             _check(t, name, dtype, ndim)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if device_status is not None:
         _check(device_status, "device_status", torch.int32)
         if device_status.get_device() != dev or device_status.numel() < 1:
@@ -390,12 +397,15 @@ def _data(t):
 
 def _pool_on(k_pages, v_pages, dev: int):
     """Shape (num_pages, Hkv, P, D) of a pool on device ``dev``."""
-    if k_pages.dim() == 4 and k_pages.dtype is torch.int8 and v_pages.dtype is torch.int8:
-        shape = n, hkv, P, D = k_pages.shape
-        if v_pages.shape == shape and k_pages.stride() == v_pages.stride() \
-                == (hkv * 2 * P * D, 2 * P * D, D, 1) and k_pages.get_device() == dev \
-                and v_pages.data_ptr() == k_pages.data_ptr() + P * D:
+    try:
+        n, hkv, P, D = shape = k_pages.shape
+        if k_pages.dtype is torch.int8 and v_pages.dtype is torch.int8 and v_pages.shape == shape \
+                and k_pages.stride() == v_pages.stride() == (hkv * 2 * P * D, 2 * P * D, D, 1) \
+                and v_pages.data_ptr() == k_pages.data_ptr() + P * D \
+                and k_pages.get_device() == dev:
             return shape
+    except (AttributeError, ValueError):
+        pass
     _check_pool(k_pages, v_pages)
     raise ValueError(f"the pool is not on the current device, cuda:{dev}")
 
@@ -460,11 +470,6 @@ def splash_release_pages(keep_lens, page_table, page_counts, free_pages, free_co
         raise SplashError(st, "splash_release_pages")
 
 
-def _strides(t):
-    """Token and head strides (0 along an axis of one: its stride says nothing)."""
-    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
-
-
 def splash_qkv_append(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, positions, slots,
                       inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                       freq_axis=None, interleaved: bool = False, rope_scale: float = 1.0,
@@ -479,18 +484,22 @@ def splash_qkv_append(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, posi
                       (inv_freq, "inv_freq", f32, 1), (q_weight, "q_weight", f32, 1),
                       (k_weight, "k_weight", f32, 1), (freq_axis, "freq_axis", i32, 1)),
                      device_status)
-    pool = num_pages, hkv, P, _ = _pool_on(k_pages, v_pages, dev)
+    pool = num_pages, hkv, P, D = _pool_on(k_pages, v_pages, dev)
     dt = q.dtype
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise TypeError("q must be float32 or bfloat16")
+    strides = []
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dtype is not dt or t.dim() != 3 or t.get_device() != dev:
             raise TypeError(f"{name} must be a 3-D {dt} tensor on cuda:{dev}")
-        if t.stride(2) != 1 and t.shape[2] > 1:
+        st = t.stride()
+        if st[2] != 1:
             raise ValueError(f"the rows of {name} must be contiguous")
-    n, hq, D = q.shape
-    if k.shape != (n, hkv, D) or v.shape != k.shape or q_out.shape != q.shape \
-            or pool[3] != D or slots.shape[0] != n or k_scales.shape != pool[:3] \
+        # along an axis of one the stride says nothing
+        strides += [st[0] if t.shape[0] > 1 else 0, st[1] if t.shape[1] > 1 else 0]
+    n, hq, _ = q.shape
+    if q_out.shape != (n, hq, D) or q_out.shape != q.shape or k.shape != (n, hkv, D) \
+            or v.shape != k.shape or slots.shape[0] != n or k_scales.shape != pool[:3] \
             or v_scales.shape != pool[:3]:
         raise ValueError("shape mismatch between q, k, v, q_out, slots and the pool")
     for w in (q_weight, k_weight):
@@ -501,15 +510,17 @@ def splash_qkv_append(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, posi
         half = inv_freq.shape[0]
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _check_all(((positions, "positions", i32, positions.dim()),), None)
-        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.dtype is not i32 or positions.get_device() != dev \
+                or not positions.is_contiguous():
+            _check_all(((positions, "positions", i32, None),), None)
+        if positions.dim() == 2:
+            axes = positions.shape[0]
         if positions.dim() not in (1, 2) or positions.shape[-1] != n or axes < 1 \
                 or (freq_axis is not None and freq_axis.shape[0] != half):
             raise ValueError("positions must be [n] or [axes, n], freq_axis one axis a frequency")
     st = LIB.splash_qkv_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dt], n, *_strides(q), *_strides(k),
-        *_strides(v), hq, hkv, D, _data(q_weight),
-        _data(k_weight), eps, _data(inv_freq), _data(freq_axis), 2 * half, int(interleaved),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dt], n, *strides, hq, hkv, D,
+        _data(q_weight), _data(k_weight), eps, _data(inv_freq), _data(freq_axis), 2 * half, int(interleaved),
         rope_scale, _data(positions) if half else None, axes, slots.data_ptr(), q_out.data_ptr(),
         k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), P,
         num_pages, _data(device_status), _raw_stream(stream, dev))
