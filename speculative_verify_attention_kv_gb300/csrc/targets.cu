@@ -751,11 +751,11 @@ __global__ void __launch_bounds__(1024) history_reset_kernel(HistoryParams p, in
   const int end = counted_end(p, b, &lo, threadIdx.x == 0 && lo_v == 0);
   const int top = min(hi_v, p.vocab);
   constexpr int kAhead = 8;          // tokens whose loads are in flight
-  for (int i = lo + threadIdx.x; i < end; i += kAhead * blockDim.x) {
+  for (long long i = lo + (long long)threadIdx.x; i < end; i += kAhead * blockDim.x) {
     int v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const long long j = (long long)i + u * blockDim.x;
+      const long long j = i + u * blockDim.x;
       v[u] = j < end ? p.tokens[j] : -1;
     }
 #pragma unroll

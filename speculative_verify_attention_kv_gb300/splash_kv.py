@@ -385,6 +385,12 @@ def _check_all(specs, device_status) -> int:
     return dev
 
 
+def _tensors(**named) -> None:
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+
 def _raw_stream(stream, dev: int) -> int:
     # the raw handle: a Stream object for the current stream costs 2.8 us of
     # host time a call, a fifth of a small call's whole
@@ -404,7 +410,7 @@ def _pool_on(k_pages, v_pages, dev: int):
                 and v_pages.data_ptr() == k_pages.data_ptr() + P * D \
                 and k_pages.get_device() == dev:
             return shape
-    except (AttributeError, ValueError):
+    except ValueError:                           # not four dimensions
         pass
     _check_pool(k_pages, v_pages)
     raise ValueError(f"the pool is not on the current device, cuda:{dev}")
@@ -478,6 +484,7 @@ def splash_qkv_append(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, posi
     quantised append. ``q``, ``k``, ``v``: float32 or bfloat16 [n, heads, D],
     strided views with contiguous rows. ``positions``: int32 [n] or [axes, n]
     (None without a rotation)."""
+    _tensors(q=q, k=k, v=v, k_pages=k_pages, v_pages=v_pages)
     f32, i32 = torch.float32, torch.int32
     dev = _check_all(((q_out, "q_out", torch.bfloat16, 3), (k_scales, "k_scales", f32, 3),
                       (v_scales, "v_scales", f32, 3), (slots, "slots", i32, 1),
@@ -510,7 +517,7 @@ def splash_qkv_append(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, posi
         half = inv_freq.shape[0]
         if positions is None:
             raise ValueError("a rotation needs positions")
-        if positions.dtype is not i32 or positions.get_device() != dev \
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not i32 or positions.get_device() != dev \
                 or not positions.is_contiguous():
             _check_all(((positions, "positions", i32, None),), None)
         if positions.dim() == 2:
@@ -532,6 +539,7 @@ def splash_kv_gather(k_pages, v_pages, k_scales, v_scales, slots, k_out, v_out,
                      device_status=None, stream=None) -> None:
     """Dequantised cached rows: ``k_out`` / ``v_out`` float32 or bfloat16
     [n, Hkv, D]; rows with slot -1 are left as they were."""
+    _tensors(k_out=k_out, k_pages=k_pages, v_pages=v_pages)
     dt = k_out.dtype
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise TypeError("k_out must be float32 or bfloat16")
@@ -602,6 +610,7 @@ def splash_choose_targets(logits, q_offsets, target_tokens, workspace, max_block
     """``logits``: float32, bfloat16 or float16 [n, vocab] with contiguous rows
     (a view of wider rows is fine); ``mask``: int32 [masks, >= ceil(vocab/32)];
     ``out``: float32 [n, vocab], possibly ``logits`` itself."""
+    _tensors(logits=logits)
     f32, i32 = torch.float32, torch.int32
     dev = _check_all(((q_offsets, "q_offsets", i32, 1), (target_tokens, "target_tokens", i32, 1),
                       (workspace, "workspace", torch.uint8, 1),
@@ -635,7 +644,7 @@ def splash_choose_targets(logits, q_offsets, target_tokens, workspace, max_block
         raise ValueError("shape mismatch between the bias tensors")
     if mask_rows is not None and (mask is None or mask_rows.shape[0] != n):
         raise ValueError("mask_rows has one entry a row and needs mask")
-    if out is not None and (out.dtype is not f32 or out.get_device() != dev
+    if out is not None and (not isinstance(out, torch.Tensor) or out.dtype is not f32 or out.get_device() != dev
                             or tuple(out.shape) != (n, vocab)
                             or (out.stride(1) != 1 and vocab > 1)):
         raise ValueError("out must be float32 [n, vocab] with contiguous rows")

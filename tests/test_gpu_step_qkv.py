@@ -274,6 +274,31 @@ def test_the_append_agrees_with_kv_append():
     assert all(torch.equal(a, b) for a, b in zip(old, new))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_codes_next_to_rounding_borders(D):
+    """Values within a few ulps of (k + 1/2) steps, for scales of many sizes: the
+    codes of both appends are those of the division, bit for bit."""
+    r = np.random.default_rng(D)
+    n, hkv = 64, 2
+    a = np.exp2(r.uniform(-120, 120, (n, hkv, 1))).astype(np.float32)
+    a[:8] = np.exp2(r.integers(-149, -120, (8, hkv, 1))).astype(np.float32)      # subnormal steps
+    s = (a / np.float32(127)).astype(np.float32)
+    k = r.integers(-127, 127, (n, hkv, D)) + 0.5
+    x = (k * s.astype(np.float64)).astype(np.float32)
+    ulps = r.integers(-3, 4, x.shape).astype(np.int32)
+    x = np.where(x == 0, x, (x.view(np.int32) + ulps).view(np.float32))
+    x = np.clip(x, -a, a)
+    x[:, :, 5] = a[:, :, 0]
+    t = torch.tensor(x, device="cuda")
+    q_out, pool, _ = run(t[:, :1].contiguous(), t, -t, i32(np.arange(n)), n // 16)
+    c = cached(pool, i32(np.arange(n)))
+    check_exact(c[0], c[2], x)
+    check_exact(c[1], c[3], -x)
+    old = pool_of(n // 16, hkv, D)
+    sk.splash_kv_append(t, -t, *old, i32([np.arange(n // 16)]), i32([0]), i32([n]))
+    assert all(torch.equal(a, b) for a, b in zip(old, pool))
+
+
 def test_q_in_place_and_on_another_stream():
     n, hq, hkv, D = 50, 8, 2, 128
     q, k, v, slots, pages = make(6, n, hq, hkv, D, torch.bfloat16, layout="separate")

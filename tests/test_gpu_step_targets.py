@@ -173,8 +173,11 @@ def test_windows_of_several_vectors():
 
 def test_a_state_full_of_tokens():
     """Every token touched: the list of special tokens is the whole window."""
-    for kind, V in (("bf16", 6000), ("f32", 3001)):
-        Scene(5, [2, 6], V, kind, dense_state=1.0).check()
+    for kind, V in (("bf16", 6000), ("f32", 3001), ("f32", 3000)):
+        s = Scene(5, [2, 6], V, kind, dense_state=1.0)
+        s.check()
+        if kind == "f32":
+            s.check(out="in place")
 
 
 def test_single_penalties_and_values_that_do_not_count():
@@ -328,3 +331,31 @@ def test_a_workspace_that_is_too_small():
     with pytest.raises(sk.SplashError) as e:
         sk.splash_choose_targets(z, q, got, torch.empty(64, dtype=torch.uint8, device="cuda"), 4)
     assert e.value.status == -3 and got.tolist() == [-7] * 4
+
+
+def test_output_rows_of_any_stride():
+    for kind, V, pad in (("bf16", 2500, 3), ("f32", 2499, 5), ("f32", 2500, 12)):
+        s = Scene(13, [3, 2], V, kind, masks="some")
+        wide = torch.full((s.n, V + pad), 77.0, device="cuda")
+        got, _, st = s.run(out=None)
+        t2 = torch.full((s.n,), -7, dtype=torch.int32, device="cuda")
+        off = np.concatenate([[0], np.cumsum([len(b) for b in s.bias])])
+        e = [x for b in s.bias for x in b]
+        sk.splash_choose_targets(
+            s.logits, i32(s.q), t2, sk.alloc_target_workspace(s.n, V), 3, block_tokens=i32(s.tokens),
+            state=torch.tensor(s.state, device="cuda").short(), repetition=f32(s.rep),
+            presence=f32(s.pres), frequency=f32(s.freq), bias_offsets=i32(off),
+            bias_ids=i32([x[0] for x in e]), bias_values=f32([x[1] for x in e]),
+            mask=torch.tensor(s.mask, device="cuda").int(), mask_rows=i32(s.rows), out=wide[:, :V])
+        assert torch.equal(got, t2) and (wide[:, V:] == 77).all()
+        assert np.array_equal(wide[:, :V].cpu().numpy(), s.want()[0])
+
+
+def test_rows_before_the_first_sequence_and_a_long_bias_list():
+    s = Scene(14, [2, 3], 900, "bf16", masks="none", nbias=0)
+    s.bias = [[(v, 0.25 * (v % 7)) for v in range(-3, 903)] * 3, []]       # every token, thrice
+    s.check()
+    # offsets that begin past row 0 leave the rows before them
+    q = torch.full((5,), -7, dtype=torch.int32, device="cuda")
+    sk.splash_choose_targets(s.logits, i32([2, 4, 5]), q, sk.alloc_target_workspace(5, 900), 2)
+    assert q.tolist() == [-7, -7] + s.logits[2:].float().argmax(-1).tolist()
