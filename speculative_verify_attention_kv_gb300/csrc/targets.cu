@@ -337,6 +337,7 @@ template <typename T>
 struct WarpSmem {
   uint32_t map[Segment<T>::kWords + 1];    // special tokens
   uint32_t block[Segment<T>::kWords + 1];  // those of the block among them
+  const uint32_t* words[kChunk];           // of the rows' masks, nullptr for none
   uint16_t list[Segment<T>::kBits];
   // the octets across a row's ends; a lane's octets that have a maximum
   alignas(16) Octet<T> stage[Segment<T>::kOctets > 2 ? Segment<T>::kOctets : 2];
@@ -371,13 +372,11 @@ choose_kernel(TargetParams p) {
   const T* z_first = static_cast<const T*>(p.logits) + first * p.stride;
   const int seg0 = run * p.span, seg1 = min(seg0 + p.span, p.segments);
 
-  // lane t: the mask words of row t, and its best choice so far
+  unsigned long long best = 0;                   // lane t: the best choice of row t so far
   const int my_mask = lane < T_b ? mask_of(p, first + lane) : kNoMask;
-  const unsigned long long my_words = my_mask >= 0 ? (unsigned long long)mask_words(p, my_mask) : 0;
-  unsigned long long best = 0;
-  auto words_of = [&](int t) {
-    return p.mask ? reinterpret_cast<const uint32_t*>(__shfl_sync(kAll, my_words, t)) : nullptr;
-  };
+  if (lane < T_b) sm.words[lane] = my_mask >= 0 ? mask_words(p, my_mask) : nullptr;
+  __syncwarp();
+  auto words_of = [&](int t) { return p.mask ? sm.words[t] : nullptr; };
   const unsigned shut = __ballot_sync(kAll, my_mask == kShut);
   auto shift_of = [&](int t) {
     return kAligned ? 0
@@ -482,9 +481,9 @@ choose_kernel(TargetParams p) {
       uint32_t word[kChunk];
     } sp;
     auto load_special = [&](int e) {
-      const bool live = e < listed;
-      sp.o = live ? sm.list[e] : 32;
+      sp.o = e < listed ? sm.list[e] : 32;
       sp.v = base + sp.o;
+      const bool live = e < listed && sp.v < V;
       sp.held = q.penal && live ? q.state[sp.v] : 0;
       sp.entry = biased && live ? s_bias[sp.o] : 0;
       sp.bias = sp.entry ? p.bias_values[q.bias0 + sp.entry - 1] : 0.f;
@@ -555,7 +554,7 @@ choose_kernel(TargetParams p) {
       if (lane == t) best = ((unsigned long long)top << 32) | (uint32_t)~at;
     };
     for (int e0 = 0; e0 == 0 || e0 < listed; e0 += 32) {
-      if (special) load_special(e0 + lane);
+      if (listed > 0) load_special(e0 + lane);
       if (e0 == 0) {
         const int block1 = (seg + 1) * S::kBlocks;
         for (int block = seg * S::kBlocks; block < block1; ++block) {
@@ -569,7 +568,7 @@ choose_kernel(TargetParams p) {
         }
         if constexpr (kOut) __syncwarp();        // the special ones' places are written
       }
-      if (!special) break;
+      if (listed == 0) break;
       // --- the special tokens ----------------------------------------------------
       const bool live = e0 + lane < listed, in_prompt = sp.held < 0;
       const bool in_block = live && (sm.block[sp.o >> 5] >> (sp.o & 31)) & 1;
