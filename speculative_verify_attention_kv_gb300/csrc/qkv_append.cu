@@ -34,6 +34,13 @@
 // 20 and 4), and the next batch's loads, of the next token at the end, are in
 // flight meanwhile. A batch is all of one kind (q, k or v). Few tokens are split
 // over more warps by batches.
+//
+// Measured, 32768 tokens of 24 + 2 x 4 heads of 256, bf16, normed and rotated (973
+// MB): 174 us, 5.6 TB/s, 82% of the measured copy rate; 106 million warp
+// instructions, 2.1 a clock (a first version with a lane to 8 columns in a row,
+// shuffled partners and divided codes: 317 us). 455 tokens: 8.1 us, a chain of
+// loads and angles. Batches of 2 rows at 20 or 24 warps to an SM: 212 us; 20 warps
+// with batches of 4 spill: 194 us.
 #include <cmath>
 #include <type_traits>
 
@@ -170,7 +177,7 @@ __device__ inline void reduce_rows(float (&v)[kB], int lane, F f) {
 }
 
 // kPaired: interleaved pairs. kFull: the whole head is rotated (known when compiled,
-// it spares every row the choice between turning and not: 193 -> 176 us for a
+// it spares every row the choice between turning and not: 193 -> 174 us for a
 // 32768-token prompt). Values are held as x[0..1] = u, x[2..3] = v of the
 // lane's pairs (in column order where the lane's columns are not rotated and
 // kPaired is false: then u is the first piece, v the second).
