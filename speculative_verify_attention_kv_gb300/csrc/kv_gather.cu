@@ -1,5 +1,5 @@
-// Cached rows back by slot: row i of k_out / v_out is code * scale of the K and
-// V rows at slots[i], for every KV head, rounded once to the output's type.
+// Cached rows back by slot: row i of k_out / v_out is the fp32 product code * scale
+// of the K and V rows at slots[i], for every KV head, rounded to the output's type.
 //
 // Pure copy with a widening, bound by HBM: 2 (D + 4) bytes read and 2 D e
 // written a (row, head). A lane takes one 16-byte piece of an output row (8 bf16
