@@ -482,8 +482,8 @@ int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* 
  *         u' = (u cos a - v sin a) * rope_scale, v' = (v cos a + u sin a) * rope_scale.
  *         inv_freq: fp32 [R/2]. positions: int32 [num_axes, num_tokens];
  *         frequency i uses axis freq_axis[i] (int32 [R/2], cut to the axes
- *         there are; NULL: axis 0). Angles are exact to 2^-32 of a turn at any
- *         32-bit position.
+ *         there are; NULL: axis 0). At any 32-bit position an angle is cut to a
+ *         multiple of 2^-32 of a turn and rounded once to fp32.
  *   q:    rounded to bf16 into q_out [num_tokens, Hq, D] (contiguous; may be q
  *         itself when q is contiguous bf16)
  *   k, v: splash_kv_append's quantiser, into slot slots[row] (page * P +

@@ -13,9 +13,9 @@
 //
 // The angle is taken modulo one turn in 64-bit fixed point: inv_freq_i / 2 pi is
 // held as F_i / 2^64 turns (its 24-bit significand times a 96-bit 1 / 2 pi,
-// shifted), and position * F_i wraps by itself. The error is below position *
-// 2^-63 turns, so far positions keep the accuracy of near ones, at the cost of
-// an integer product (fp64, the other way to it, runs at 2 FMA a clock and SM
+// shifted), and position * F_i wraps by itself, with an error below position *
+// 2^-63 turns; its upper 32 bits, rounded to fp32, are the angle. So far positions
+// keep the accuracy of near ones, at the cost of an integer product (fp64, the other way to it, runs at 2 FMA a clock and SM
 // here). sincospif then needs no range reduction.
 //
 // A warp takes one token and a run of its heads, 8 values a lane (so a head of
