@@ -15,8 +15,9 @@
 // held as F_i / 2^64 turns (its 24-bit significand times a 96-bit 1 / 2 pi,
 // shifted), and position * F_i wraps by itself, with an error below position *
 // 2^-63 turns; its upper 32 bits, rounded to fp32, are the angle. So far positions
-// keep the accuracy of near ones, at the cost of an integer product (fp64, the other way to it, runs at 2 FMA a clock and SM
-// here). sincospif then needs no range reduction.
+// keep the accuracy of near ones, at the cost of an integer product (fp64, the
+// other way to it, runs at 2 FMA a clock and SM here). sincospif then needs no
+// range reduction.
 //
 // A warp takes one token and a run of its heads, 8 values a lane (so a head of
 // D values takes D/8 lanes, and a warp 256/D heads at once). The 8 values are two
