@@ -388,3 +388,17 @@ def test_no_rows_is_no_work():
     sk.splash_kv_gather(*pool, i32([]), e, e.clone())
     sk.splash_qkv_append(e, e, e, e.clone(), *pool, None, i32([]))
     assert sk.splash_launch_count() == before
+
+
+def test_rows_further_apart_than_32_bits():
+    """Token strides past 2^31 values."""
+    n, far, D = 3, 2 ** 31 + 64, 128
+    q, k, v, slots, pages = make(10, n, 4, 1, D, torch.bfloat16)
+    wide = torch.empty(2 * far + 6 * D, dtype=torch.bfloat16, device="cuda")
+    row = wide.as_strided((n, 6, D), (far, D, 1))
+    row[:, :4], row[:, 4:5], row[:, 5:] = q, k, v
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    f = torch.rand(D // 2, device="cuda")
+    want, wpool, _ = run(q, k, v, slots, pages, pos, inv_freq=f)
+    got, gpool, _ = run(row[:, :4], row[:, 4:5], row[:, 5:], slots, pages, pos, inv_freq=f)
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(gpool, wpool))

@@ -359,3 +359,30 @@ def test_rows_before_the_first_sequence_and_a_long_bias_list():
     q = torch.full((5,), -7, dtype=torch.int32, device="cuda")
     sk.splash_choose_targets(s.logits, i32([2, 4, 5]), q, sk.alloc_target_workspace(5, 900), 2)
     assert q.tolist() == [-7, -7] + s.logits[2:].float().argmax(-1).tolist()
+
+
+@pytest.mark.parametrize("kind,in_place", [("bf16", False), ("f32", False), ("f32", True)])
+def test_rows_further_apart_than_32_bits(kind, in_place):
+    """Row strides past 2^31 values: five rows begin up to 2^33 values apart."""
+    T, V, far = [2, 3], 2500, 2 ** 31 + 8
+    s = Scene(21, T, V, kind)
+    wide = torch.empty(4 * far + V, dtype=KINDS[kind], device="cuda")
+    rows = wide.as_strided((5, V), (far, 1))
+    rows.copy_(s.logits)
+    s.logits = rows
+    z, pick = s.want()
+    out = rows if in_place else torch.full((5, V), 77.0, device="cuda")
+    off = np.concatenate([[0], np.cumsum([len(b) for b in s.bias])])
+    e = [x for b in s.bias for x in b]
+    got = torch.full((5,), -7, dtype=torch.int32, device="cuda")
+    sk.splash_choose_targets(rows, i32(s.q), got, sk.alloc_target_workspace(5, V), 3, i32(s.tokens),
+                             torch.tensor(s.state, device="cuda").short(), f32(s.rep), f32(s.pres),
+                             f32(s.freq), i32(off), i32([x[0] for x in e]), f32([x[1] for x in e]),
+                             torch.tensor(s.mask, device="cuda").int(), out=out)
+    assert np.array_equal(got.cpu().numpy(), pick)
+    assert np.array_equal(out.cpu().numpy(), z)
+
+
+@pytest.mark.parametrize("T,V", [([128] * 3, 5000), ([1] * 300, 1500), ([127, 1, 0, 64], 131072)])
+def test_the_longest_blocks_and_many_sequences_of_one_row(T, V):
+    Scene(22, T, V, "bf16", masks="some", tail=2).check()
