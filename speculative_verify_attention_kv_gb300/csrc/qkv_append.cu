@@ -32,16 +32,21 @@
 // pairs of fp32 (f32x2); the weight is folded into the token's cosines and sines.
 // A batch of kB head rows is worked on together: their kB sums of squares are
 // reduced in one exchange pattern (6 shuffles and one root for 4 rows instead of
-// 20 and 4), and the next batch's loads, of the next token at the end, are in
-// flight meanwhile. A batch is all of one kind (q, k or v). Few tokens are split
-// over more warps by batches.
+// 20 and 4). A batch is all of one kind (q, k or v). Few tokens are split over more
+// warps by batches.
+//
+// The loads run ahead: each warp has a ring of kStages batches in shared memory,
+// filled by cp.async across the ends of tokens, two batches (4 KB) in flight under
+// the one worked on. A lane reads only what it copied, so the ring needs no barrier.
 //
 // Measured, 32768 tokens of 24 + 2 x 4 heads of 256, bf16, normed and rotated (973
-// MB): 174 us, 5.6 TB/s, 82% of the measured copy rate; 106 million warp
-// instructions, 2.1 a clock (a first version with a lane to 8 columns in a row,
-// shuffled partners and divided codes: 317 us). 455 tokens: 8.1 us, a chain of
-// loads and angles. Batches of 2 rows at 20 or 24 warps to an SM: 212 us; 20 warps
-// with batches of 4 spill: 194 us.
+// MB): 158 us, 6.2 TB/s, 91% of the measured copy rate. One batch ahead in registers
+// instead of the ring: 174 us (a first version with a lane to 8 columns in a row,
+// shuffled partners and divided codes: 317 us). 2, 4 and 6 stages 173, 160 and 160
+// us; with fp32 inputs 3 stages 228 us, 4 245 us. Batches of 2 rows at 16, 20 or 24
+// warps to an SM: 174, 180, 181 us; 20 warps with batches of 4 spill: 193 us. Heads
+// of 128 98 us and of 64 73 us for the same tokens: there the instructions bound it.
+// 455 tokens: 8.2 us, a chain of loads and angles.
 #include <cmath>
 #include <type_traits>
 
@@ -57,9 +62,10 @@ constexpr int kQkvWarps = 4;
 constexpr int kQkvThreads = 32 * kQkvWarps;
 constexpr int kEpl = 8;          // values a lane holds of a head row
 constexpr int kWarpsPerSm = 16;  // resident: what the registers leave room for
-// Head rows of a batch: 64 bytes a lane in flight
+// Head rows of a batch: 64 bytes a lane
 template <typename T>
 constexpr int kBatch = 8 / sizeof(T);
+constexpr int kStages = 3;         // batches of a warp's ring
 
 struct QkvParams {
   const void* q;
@@ -89,24 +95,43 @@ struct QkvParams {
   int* status;
 };
 
-// A lane's 8 values of a row as they are stored: two pieces of 4.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<__nv_bfloat16> {
-  uint2 a, b;
-  __device__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
-    a = *reinterpret_cast<const uint2*>(p);
-    b = *reinterpret_cast<const uint2*>(q);
+// A copy of kBytes to shared memory in the background; zeros where not `live`.
+template <int kBytes>
+__device__ inline void copy_async(uint32_t dst, const void* src, bool live) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(live ? kBytes : 0) : "memory");
+}
+__device__ inline void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups of copies but the last kOpen have arrived.
+template <int kOpen>
+__device__ inline void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kOpen) : "memory");
+}
+
+// A lane's 8 values of a row, two pieces of 4 at p and q (kPaired: 8 from p on),
+// on their way through shared memory. A lane reads only what it copied itself.
+// at: of the warp's row there.
+template <typename T, bool kPaired>
+struct Piece;
+template <bool kPaired>
+struct Piece<__nv_bfloat16, kPaired> {
+  static constexpr int kBytes = 512;             // of a warp's row
+  __device__ static void copy(uint32_t at, int lane, const __nv_bfloat16* p,
+                              const __nv_bfloat16* q, bool live) {
+    if constexpr (kPaired) {
+      copy_async<16>(at + lane * 16, p, live);
+    } else {
+      copy_async<8>(at + lane * 16, p, live);
+      copy_async<8>(at + lane * 16 + 8, q, live);
+    }
   }
-  __device__ void load8(const __nv_bfloat16* p) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    a = make_uint2(w.x, w.y);
-    b = make_uint2(w.z, w.w);
-  }
-  __device__ void zero() { a = b = make_uint2(0, 0); }
-  __device__ void get(float (&x)[kEpl]) const {
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+  __device__ static void get(const unsigned char* at, int lane, float (&x)[kEpl]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at + lane * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -114,16 +139,16 @@ struct Raw<__nv_bfloat16> {
     }
   }
 };
-template <>
-struct Raw<float> {
-  float4 a, b;
-  __device__ void load(const float* p, const float* q) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(q);
+template <bool kPaired>
+struct Piece<float, kPaired> {
+  static constexpr int kBytes = 1024;
+  __device__ static void copy(uint32_t at, int lane, const float* p, const float* q, bool live) {
+    copy_async<16>(at + lane * 16, p, live);
+    copy_async<16>(at + 512 + lane * 16, q, live);
   }
-  __device__ void load8(const float* p) { load(p, p + 4); }
-  __device__ void zero() { a = b = make_float4(0, 0, 0, 0); }
-  __device__ void get(float (&x)[kEpl]) const {
+  __device__ static void get(const unsigned char* at, int lane, float (&x)[kEpl]) {
+    const float4 a = *reinterpret_cast<const float4*>(at + lane * 16);
+    const float4 b = *reinterpret_cast<const float4*>(at + 512 + lane * 16);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
@@ -214,8 +239,12 @@ qkv_append_kernel(QkvParams p) {
     }
   };
 
-  // Batch `bi` of token `tok`: rows past the last head are zero.
-  auto load = [&](Raw<TIn> (&raw)[kB], int tok, int bi) {
+  using Row = Piece<TIn, kPaired>;
+  __shared__ __align__(16) unsigned char s_ring[kQkvWarps][kStages][kB * Row::kBytes];
+  unsigned char (*ring)[kB * Row::kBytes] = s_ring[threadIdx.x >> 5];
+  // Batch `bi` of token `tok` to a stage of the ring; rows past the last head are
+  // zero.
+  auto copy = [&](int stage, int tok, int bi) {
     const TIn* base;
     long long head;
     int h0, heads;
@@ -230,11 +259,12 @@ qkv_append_kernel(QkvParams p) {
       base = static_cast<const TIn*>(p.v) + tok * p.v_tok;
     }
     const TIn* row = base + (h0 + hl) * head;
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring[stage]);
 #pragma unroll
     for (int u = 0; u < kB; ++u) {
-      if (h0 + u * kRows + hl >= heads) raw[u].zero();
-      else if constexpr (kPaired) raw[u].load8(row + ca);
-      else raw[u].load(row + ca, row + cb);
+      const bool live = h0 + u * kRows + hl < heads;
+      const TIn* from = live ? row : base;
+      Row::copy(at + u * Row::kBytes, lane, from + ca, from + cb, live);
       row += kRows * head;
     }
   };
@@ -245,24 +275,44 @@ qkv_append_kernel(QkvParams p) {
   auto batch_of = [&](unsigned item) {
     return per_token == 1 ? 0 : (int)(item % per_token) * p.batches_per_item;
   };
+  const int batches = nq + 2 * nk;
   unsigned item = blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
-  Raw<TIn> raw[kB];
-  if (item < items) load(raw, token_of(item), batch_of(item));
+  // The next batch to copy, kStages - 1 ahead of the one worked on
+  unsigned next = item;
+  int next_tok = 0, next_b = 0, next_end = 0, stage_in = 0, stage = 0;
+  auto next_item = [&] {
+    if (next >= items) return;
+    next_tok = token_of(next);
+    next_b = batch_of(next);
+    next_end = min(next_b + p.batches_per_item, batches);
+  };
+  auto copy_next = [&] {
+    if (next < items) {
+      copy(stage_in, next_tok, next_b);
+      if (++next_b == next_end) {
+        next += step;
+        next_item();
+      }
+    }
+    copies_end();
+    stage_in = stage_in == kStages - 1 ? 0 : stage_in + 1;
+  };
+  next_item();
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) copy_next();
 
   for (; item < items; item += step) {
     const int tok = token_of(item), b0 = batch_of(item);
-    const int b1 = min(b0 + p.batches_per_item, nq + 2 * nk);
+    const int b1 = min(b0 + p.batches_per_item, batches);
     const int slot = p.slots[tok];
     const int page = slot / kPageSize, at = slot % kPageSize;
-    // the batch after `bi`, of the next item at the end of this one
-    auto load_after = [&](int bi) {
-      const unsigned next = item + step;
-      if (bi + 1 < b1) load(raw, tok, bi + 1);
-      else if (next < items) load(raw, token_of(next), batch_of(next));
-    };
     if (slot < 0 || page >= p.num_pages) {       // a padded row: nothing is written
       if (slot >= 0 && lane == 0) report(p.status, SPLASH_DEVICE_BAD_PAGE);
-      load_after(b1);
+      for (int bi = b0; bi < b1; ++bi) {
+        copies_wait<kStages - 2>();
+        copy_next();
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+      }
       continue;
     }
 
@@ -313,10 +363,11 @@ qkv_append_kernel(QkvParams p) {
                        float* scale) {
       constexpr bool kKv = decltype(kv)::value;
       F2 x[kB][4];
+      copies_wait<kStages - 2>();
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
         float y[kEpl];
-        raw[u].get(y);
+        Row::get(ring[stage] + u * Row::kBytes, lane, y);
         if constexpr (kPaired) {
           x[u][0] = f2(y[0], y[2]); x[u][1] = f2(y[4], y[6]);
           x[u][2] = f2(y[1], y[3]); x[u][3] = f2(y[5], y[7]);
@@ -325,7 +376,8 @@ qkv_append_kernel(QkvParams p) {
           x[u][2] = f2(y[4], y[5]); x[u][3] = f2(y[6], y[7]);
         }
       }
-      load_after(bi);
+      copy_next();                               // to the stage read before this one
+      stage = stage == kStages - 1 ? 0 : stage + 1;
       if (turned) {
         float ss[kB];
         if (weight) {
