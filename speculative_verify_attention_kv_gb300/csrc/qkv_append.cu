@@ -45,7 +45,7 @@
 // shuffled partners and divided codes: 317 us). 2, 4 and 6 stages 173, 160 and 160
 // us; with fp32 inputs 3 stages 228 us, 4 245 us. Batches of 2 rows at 16, 20 or 24
 // warps to an SM: 174, 180, 181 us; 20 warps with batches of 4 spill: 193 us. Heads
-// of 128 98 us and of 64 73 us for the same tokens: there the instructions bound it.
+// of 128 98 us and of 64 66 us for the same tokens: there the instructions bound it.
 // 455 tokens: 8.2 us, a chain of loads and angles.
 #include <cmath>
 #include <type_traits>
@@ -62,9 +62,13 @@ constexpr int kQkvWarps = 4;
 constexpr int kQkvThreads = 32 * kQkvWarps;
 constexpr int kEpl = 8;          // values a lane holds of a head row
 constexpr int kWarpsPerSm = 16;  // resident: what the registers leave room for
-// Head rows of a batch: 64 bytes a lane
+// Warp-wide rows of a batch: 64 bytes a lane. A row of heads of 64 values is 4
+// heads already; batches of 2 leave fewer rows without a head: 24 + 2 x 4 heads 66 us
+// instead of 73, 32 + 2 x 8 heads 85 instead of 86 (32768 tokens).
 template <typename T>
-constexpr int kBatch = 8 / sizeof(T);
+constexpr int batch_rows(int head_dim) {
+  return head_dim == 64 ? 2 : 8 / (int)sizeof(T);
+}
 constexpr int kStages = 3;         // batches of a warp's ring
 
 struct QkvParams {
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kQkvThreads, kWarpsPerSm / kQkvWarps)
 qkv_append_kernel(QkvParams p) {
   constexpr int kLanes = D / kEpl;               // lanes of a head row
   constexpr int kRows = 32 / kLanes;             // head rows of a warp-wide load
-  constexpr int kB = kBatch<TIn>;
+  constexpr int kB = batch_rows<TIn>(D);
   constexpr int kHeads = kB * kRows;             // heads of a batch
   const int lane = threadIdx.x & 31, l = lane % kLanes, hl = lane / kLanes;
   const int nq = (p.hq + kHeads - 1) / kHeads, nk = (p.hkv + kHeads - 1) / kHeads;
@@ -556,7 +560,9 @@ extern "C" int splash_qkv_append(
 
   const int sms = device_sm_count();
   if (sms <= 0) return SPLASH_ERR_CUDA;
-  const int heads = (dtype == SPLASH_F32 ? kBatch<float> : kBatch<__nv_bfloat16>) * (32 * kEpl / head_dim);
+  const int heads = (dtype == SPLASH_F32 ? batch_rows<float>(head_dim)
+                                         : batch_rows<__nv_bfloat16>(head_dim)) *
+                    (32 * kEpl / head_dim);
   const int batches = (num_q_heads + heads - 1) / heads + 2 * ((num_kv_heads + heads - 1) / heads);
   // A token's heads stay with one warp while there are tokens enough to fill the
   // GPU; fewer are split by batches. More items than warps fit at once are taken
