@@ -50,6 +50,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "splash_async.cuh"
 #include "splash_common.cuh"
 #include "splash_host.cuh"
 #include "splash_quant.cuh"
@@ -99,23 +100,6 @@ struct QkvParams {
   int* status;
 };
 
-// A copy of kBytes to shared memory in the background; zeros where not `live`.
-template <int kBytes>
-__device__ inline void copy_async(uint32_t dst, const void* src, bool live) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
-                 "r"(live ? kBytes : 0) : "memory");
-}
-__device__ inline void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All groups of copies but the last kOpen have arrived.
-template <int kOpen>
-__device__ inline void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kOpen) : "memory");
-}
-
 // A lane's 8 values of a row, two pieces of 4 at p and q (kPaired: 8 from p on),
 // on their way through shared memory. A lane reads only what it copied itself.
 // at: of the warp's row there.
@@ -127,10 +111,10 @@ struct Piece<__nv_bfloat16, kPaired> {
   __device__ static void copy(uint32_t at, int lane, const __nv_bfloat16* p,
                               const __nv_bfloat16* q, bool live) {
     if constexpr (kPaired) {
-      copy_async<16>(at + lane * 16, p, live);
+      copy_async<16>(at + lane * 16, p, live ? 16 : 0);
     } else {
-      copy_async<8>(at + lane * 16, p, live);
-      copy_async<8>(at + lane * 16 + 8, q, live);
+      copy_async<8>(at + lane * 16, p, live ? 8 : 0);
+      copy_async<8>(at + lane * 16 + 8, q, live ? 8 : 0);
     }
   }
   __device__ static void get(const unsigned char* at, int lane, float (&x)[kEpl]) {
@@ -147,8 +131,8 @@ template <bool kPaired>
 struct Piece<float, kPaired> {
   static constexpr int kBytes = 1024;
   __device__ static void copy(uint32_t at, int lane, const float* p, const float* q, bool live) {
-    copy_async<16>(at + lane * 16, p, live);
-    copy_async<16>(at + 512 + lane * 16, q, live);
+    copy_async<16>(at + lane * 16, p, live ? 16 : 0);
+    copy_async<16>(at + 512 + lane * 16, q, live ? 16 : 0);
   }
   __device__ static void get(const unsigned char* at, int lane, float (&x)[kEpl]) {
     const float4 a = *reinterpret_cast<const float4*>(at + lane * 16);
@@ -263,7 +247,7 @@ qkv_append_kernel(QkvParams p) {
       base = static_cast<const TIn*>(p.v) + tok * p.v_tok;
     }
     const TIn* row = base + (h0 + hl) * head;
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring[stage]);
+    const uint32_t at = shared_address(ring[stage]);
 #pragma unroll
     for (int u = 0; u < kB; ++u) {
       const bool live = h0 + u * kRows + hl < heads;

@@ -19,29 +19,29 @@
 // instructions and latency: a step's rows are few, and everything before the
 // logits (offsets, state, biases, masks) is a chain of loads. So a warp works for
 // itself, without block barriers: it takes a run of segments of the vocabulary
-// (1024 tokens) for up to kChunk rows of a sequence, and the next row's or
-// segment's loads are in flight while it works on one. Of a segment only few
-// tokens are touched by a penalty or a bias ("special"). It marks them in a
-// bitmap, then
-//   - streams the rows and takes only a maximum, of the logits as they are stored:
-//     excluded tokens (special ones, and those that the mask closes) become -inf
-//     by one logic operation a register, 16-bit types stay packed in pairs, and
-//     the place of a maximum is looked up only where it beats the run's best;
-//   - does the special tokens exactly, a token a lane; the loads of the first 32
-//     of them run under the dense pass.
+// (1024 tokens) for up to kChunk rows of a sequence. Of a segment only few tokens
+// are touched by a penalty or a bias ("special"). It marks them in a bitmap, lists
+// them and fetches what they need, a token a lane. Then, a row of a block after the
+// other, with the next one's logits and mask on their way to shared memory:
+//   - it takes the maximum of the logits as they are stored: excluded tokens
+//     (special ones, and those that the mask closes) become -inf by one logic
+//     operation a register, and 16-bit types stay packed in pairs;
+//   - it computes the special tokens exactly, from the copy in shared memory;
+//   - the place of the larger of both is looked up only where it beats the run's
+//     best.
 // Choices are 64-bit keys (ordered value, complement of the index) merged by
 // maximum, which no order changes; a second kernel takes each row's maximum over
 // its runs.
 //
 // Measured, 16 x 16 rows of 131072 bf16 logits with 2.6% of special tokens and
-// half of the rows masked (73 MB): 34 us (2.2 TB/s); without penalties, biases and
-// masks 17.9 us (3.7 TB/s). 426 rows of 100003 fp32 with masks and output (359 MB):
-// 81 us (4.4 TB/s). A CTA to a window of 4096 or 8192 tokens with block barriers
-// took 33 and 82 us, 72 us instead of 57 at 256 sequences of one row; dense and
-// special CTAs side by side 33 and 147; rows in chunks of 8 33 and 95 (long and
-// short blocks do not end together). More than 16 warps to an SM spill: 20 warps
-// 47 us and more. 17.1 million warp instructions at 1.74 a clock: 9.5 million are
-// the dense pass, the rest marking, listing and doing the special tokens.
+// half of the rows masked (73 MB): 32 us (2.3 TB/s); without biases and masks 26 us;
+// without penalties too 20 us (3.4 TB/s). 426 rows of 100003 fp32 with masks and
+// output (359 MB): 78 us (4.6 TB/s), as bf16 without output 45 us. The rows in
+// registers, one ahead, and the special tokens of the chunk's rows together from
+// global memory: 34, 29, 18, 81 and 50 us. Three stages 34 and 78 us; 20 warps to an
+// SM (96 registers) 32 and 80 us. A CTA to a window of 4096 or 8192 tokens with block
+// barriers 33 and 82 us; dense and special CTAs side by side 33 and 147; rows in
+// chunks of 8 33 and 95 (long and short blocks do not end together).
 //
 // Rows of an odd vocabulary start at any alignment. Each row's vector grid is
 // shifted to its own 16-byte boundary and its segments with it, so the loads stay
@@ -50,6 +50,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "splash_async.cuh"
 #include "splash_common.cuh"
 #include "splash_host.cuh"
 
@@ -130,10 +131,6 @@ template <>
 struct Octet<float> {
   uint4 a, b;
   static constexpr uint32_t kNone = 0xff800000u;      // -inf
-  __device__ void load(const float* z) {
-    a = reinterpret_cast<const uint4*>(z)[0];
-    b = reinterpret_cast<const uint4*>(z)[1];
-  }
   __device__ static void drop4(uint4& w, uint32_t keep) {
     const uint32_t s = spread4(keep);
     w.x = keep_or(w.x, signs<0x8888>(s), kNone);
@@ -164,7 +161,6 @@ template <typename T, typename T2, uint32_t kPairNone>
 struct Octet16 {
   uint4 a;
   static constexpr uint32_t kNone = kPairNone;
-  __device__ void load(const T* z) { a = *reinterpret_cast<const uint4*>(z); }
   __device__ void drop(uint32_t keep) {
     const uint32_t s = spread4(keep), t = spread4(keep >> 4);
     a.x = keep_or(a.x, signs<0x9988>(s), kNone);
@@ -268,8 +264,8 @@ __device__ inline uint32_t touched(const uint4& w) {
 template <typename T>
 struct Segment {
   static constexpr int kTokens = 1024;
-  static constexpr int kOctets = 8 / sizeof(T);  // a lane's of a row in flight: 64 bytes
-  static constexpr int kBlock = 32 * 8 * kOctets;        // tokens of a row in flight
+  static constexpr int kOctets = 8 / sizeof(T);  // a lane's of a block: 64 bytes
+  static constexpr int kBlock = 32 * 8 * kOctets;        // tokens of a block: 2 KB of a row
   static constexpr int kBlocks = kTokens / kBlock;
   static constexpr int kEarly = 16 / sizeof(T) - 1;
   // The bitmap begins 32 tokens before the segment: a shifted row's segment
@@ -278,65 +274,60 @@ struct Segment {
   static constexpr int kWords = kBits / 32;
 };
 
-// A lane's octets of a row: the logits, and the words of the row's mask that hold
-// their bits (all ones without a mask). Octet n starts 256 tokens, 8 words, after
-// the one before it, so a bit's place in its word is the same for all n. kAligned:
-// every row begins on 16 bytes, and an octet's bits never cross a word.
-template <typename T, bool kAligned>
-struct RowVecs {
-  static constexpr int N = Segment<T>::kOctets;
-  Octet<T> raw[N];
-  uint32_t w0[N], w1[N];
+// A block of a row on its way through shared memory: the logits from token g0 on and
+// the words of the row's mask from word g0 / 32 on. What lies outside the row is
+// undefined there.
+constexpr int kStages = 2;           // one row ahead
+template <typename T>
+struct Stage {
+  static constexpr int kWords = Segment<T>::kBlock / 32 + 1;
+  alignas(16) Octet<T> raw[32 * Segment<T>::kOctets];
+  uint32_t mask[kWords + 1];                     // the last one is read, not used
 
-  // z, q: where octet 0 and the mask word of its first token v0 are; q == nullptr:
-  // no mask. Every octet lies inside the row.
-  __device__ void load(const T* z, const uint32_t* q, int v0) {
+  // Starts the copies of the warp; the row is z_row[0, V). Its 16-byte pieces are
+  // the row's own: one at most crosses each end.
+  template <bool kAligned>
+  __device__ void copy(const T* z_row, const uint32_t* mask_row, int g0, int V, int lane) {
+    constexpr int E = 16 / sizeof(T), kPieces = Segment<T>::kBlock / E / 32;
+    const T* src = z_row + (g0 + lane * E);
+    const uint32_t dst = shared_address(raw) + lane * 16;
+    if ((kAligned || g0 >= 0) && g0 + Segment<T>::kBlock <= V) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) raw[n].load(z + n * 256);
+      for (int i = 0; i < kPieces; ++i) copy_async<16>(dst + i * 512, src + i * 32 * E, 16);
+    } else {
 #pragma unroll
-    for (int n = 0; n < N; ++n) w0[n] = w1[n] = kAll;
-    if (q) {
+      for (int i = 0; i < kPieces; ++i) {
+        const int v = g0 + (i * 32 + lane) * E;
+        if (v >= 0 && v < V)
+          copy_async<16>(dst + i * 512, src + i * 32 * E, min(V - v, E) * (int)sizeof(T));
+      }
+      if (!kAligned && g0 < 0 && lane < E && g0 + lane >= 0 && g0 + lane < V)
+        reinterpret_cast<T*>(raw)[lane] = z_row[g0 + lane];
+    }
+    if (mask_row) {
+      const int words = (V + 31) >> 5, w0 = g0 >> 5;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        w0[n] = q[n * 8];
-        if (!kAligned && (v0 & 31) > 24) w1[n] = q[n * 8 + 1];
+      for (int i = 0; i < kWords; i += 32) {
+        const int w = w0 + i + lane;
+        if (i + lane < kWords && w >= 0 && w < words)
+          copy_async<4>(shared_address(mask + i + lane), mask_row + w, 4);
       }
     }
   }
-  // The same where octets may cross an end of the row or lie past it. z_row, mask:
-  // of the row; g0: v0 of lane 0. One octet crosses each end at most: its values
-  // come one a lane, by way of shared memory.
-  __device__ void load_end(const T* z_row, const uint32_t* mask, int g0, int V, Octet<T>* stage,
-                           int lane) {
-    const int high = g0 + ((V - g0) & ~7);       // the octet that the row's end is in
-    const int e = lane < 8 ? g0 + lane : high + lane - 8;
-    T one{};
-    if (lane < 16 && e >= 0 && e < V) one = z_row[e];
-    const int words = (V + 31) >> 5;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int v = g0 + lane * 8 + n * 256, sh = v & 31, w = v >> 5;
+  // The bits of octet n, token v on, that are in the row and open in its mask
+  // (upper bits: others').
+  template <bool kAligned>
+  __device__ uint32_t open(int v, int g0, int V, bool masked) const {
+    uint32_t on = kAll;
+    if (masked) {
+      const int i = (v >> 5) - (g0 >> 5);
+      on = kAligned ? mask[i] >> (v & 31) : __funnelshift_r(mask[i], mask[i + 1], v & 31);
+    }
+    if ((!kAligned && g0 < 0) || g0 + Segment<T>::kBlock > V) {
       const int from = v < 0 ? -v : 0, to = V - v < 8 ? V - v : 8;
-      if (v >= 0 && v + 8 <= V) raw[n].load(z_row + v);
-      uint32_t on = to > 0 && from < 8 ? ((1u << to) - 1) & ~((1u << from) - 1) : 0;
-      if (mask && on)
-        on &= __funnelshift_r(w >= 0 && w < words ? mask[w] : 0u,
-                              w + 1 >= 0 && w + 1 < words ? mask[w + 1] : 0u, sh);
-      w0[n] = on << sh;
-      w1[n] = sh ? on >> (32 - sh) : 0;
+      on &= to > 0 && from < 8 ? ((1u << to) - 1) & ~((1u << from) - 1) : 0;
     }
-    __syncwarp();
-    if (lane < 16) reinterpret_cast<T*>(stage)[lane] = one;
-    __syncwarp();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int v = g0 + lane * 8 + n * 256;
-      if (v < 0 || v + 8 > V) raw[n] = stage[v == high ? 1 : 0];
-    }
-  }
-  // The mask bits of octet n (upper bits: others')
-  __device__ uint32_t bits(int n, int v0) const {
-    return kAligned ? w0[n] >> (v0 & 31) : __funnelshift_r(w0[n], w1[n], v0 & 31);
+    return on;
   }
 };
 
@@ -348,15 +339,14 @@ struct WarpSmem {
   uint32_t block[Segment<T>::kWords + 1];  // those of the block among them
   const uint32_t* words[kChunk];           // of the rows' masks, nullptr for none
   uint16_t list[Segment<T>::kBits];
-  // the octets across a row's ends; a lane's octets that have a maximum
-  alignas(16) Octet<T> stage[Segment<T>::kOctets > 2 ? Segment<T>::kOctets : 2];
+  alignas(16) Octet<T> top[Segment<T>::kOctets]; // a lane's octets that have a maximum
+  Stage<T> ring[kStages];
 };
 
 template <typename T, bool kOut, bool kAligned>
 __global__ void __launch_bounds__(32 * kWarpsPerCta, 16 / kWarpsPerCta)
 choose_kernel(TargetParams p) {
   using S = Segment<T>;
-  using Vecs = RowVecs<T, kAligned>;
   constexpr int N = S::kOctets;
   constexpr int kGroups = S::kTokens / 8 / 32;   // state groups of 8 entries a lane
   constexpr int kIds = 10;
@@ -391,17 +381,21 @@ choose_kernel(TargetParams p) {
     return kAligned ? 0
                     : (int)((reinterpret_cast<uintptr_t>(z_first + t * p.stride) & 15) / sizeof(T));
   };
-  // First token of this lane's octets in row t of a block (kBlocks to a segment)
-  auto first_of = [&](int block, int t) { return block * S::kBlock + lane * 8 - shift_of(t); };
-  Vecs x;                                        // the row whose loads are in flight
-  auto load_row = [&](int block, int t) {
-    const int v0 = first_of(block, t);
-    const T* z_row = z_first + t * p.stride;
-    const uint32_t* mask = words_of(t);
-    if ((kAligned || block > 0) && (block + 1) * S::kBlock <= V)
-      x.load(z_row + v0, mask ? mask + (v0 >> 5) : nullptr, v0);
-    else
-      x.load_end(z_row, mask, v0 - lane * 8, V, sm.stage, lane);
+  // First token of row t of a block (kBlocks to a segment)
+  auto first_of = [&](int block, int t) { return block * S::kBlock - shift_of(t); };
+  // The next row of a block to copy, kStages - 1 ahead of the one worked on
+  int next_block = seg0 * S::kBlocks, next_t = 0, stage_in = 0, stage = 0;
+  auto copy_next = [&] {
+    if (next_block < seg1 * S::kBlocks) {
+      sm.ring[stage_in].template copy<kAligned>(z_first + next_t * p.stride, words_of(next_t),
+                                                first_of(next_block, next_t), V, lane);
+      if (++next_t == T_b) {
+        next_t = 0;
+        ++next_block;
+      }
+    }
+    copies_end();
+    stage_in = stage_in == kStages - 1 ? 0 : stage_in + 1;
   };
   uint4 st[kGroups];
   auto load_state = [&](int seg) {
@@ -412,7 +406,8 @@ choose_kernel(TargetParams p) {
     }
   };
   if (q.penal) load_state(seg0);
-  load_row(seg0 * S::kBlocks, 0);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) copy_next();
   if (biased)
     for (int i = lane; i < S::kBits; i += 32) s_bias[i] = 0;
 
@@ -481,148 +476,147 @@ choose_kernel(TargetParams p) {
       __syncwarp();
     }
 
-    // --- a lane's first special token: its loads run under the dense pass ------
-    // Token list[e]: what its processing for rows 0 .. T_b - 1 reads.
-    struct {
-      int o, v, held, entry;
+    // --- a lane's special tokens: list[e] and what its rows need --------------
+    struct Entry {
+      int v;                                     // the token; none: before every row
+      int count;                                 // before the chunk's rows
       float bias;
-      T z[kChunk];
-      uint32_t word[kChunk];
-    } sp;
-    auto load_special = [&](int e) {
-      sp.o = e < listed ? sm.list[e] : 32;
-      sp.v = base + sp.o;
-      const bool live = e < listed && sp.v < V;
-      sp.held = q.penal && live ? q.state[sp.v] : 0;
-      sp.entry = biased && live ? s_bias[sp.o] : 0;
-      sp.bias = sp.entry ? p.bias_values[q.bias0 + sp.entry - 1] : 0.f;
-      const T* zp = z_first + sp.v;
-#pragma unroll
-      for (int t = 0; t < kChunk; ++t) {
-        if (t >= T_b) break;
-        const uint32_t* mask = words_of(t);
-        // the row's own segment is shifted with it
-        const int from = lo - shift_of(t);
-        sp.z[t] = T{};
-        sp.word[t] = 0;
-        if (live && (kAligned || (sp.v >= from && sp.v < from + S::kTokens))) {
-          sp.z[t] = *zp;
-          sp.word[t] = mask ? mask[sp.v >> 5] : kAll;
-        }
-        zp += p.stride;
-      }
+      uint32_t flags;                            // bit t: row t's token is v
     };
-    // --- dense: the largest value of every other token -------------------------
-    auto take_row = [&](Vecs& x, int block, int t) {
-      const int v0 = first_of(block, t);
-      const bool closed = (shut >> t) & 1;
+    constexpr uint32_t kPrompt = 1u << kChunk, kBias = 2u << kChunk;
+    auto entry_at = [&](int e) {
+      Entry a{INT_MIN / 4, 0, 0.f, 0};
+      const int o = e < listed ? sm.list[e] : 0, v = base + o;
+      if (e >= listed || v >= V) return a;
+      a.v = v;
+      if (q.penal) {
+        const int held = q.state[v];
+        a.count = held & 0x7fff;
+        if (held < 0) a.flags |= kPrompt;
+        if ((sm.block[o >> 5] >> (o & 31)) & 1) {
+          for (int s = 0; s < skip; ++s) a.count += p.tokens[q.first + s] == v;
+          for (int t = 0; t < T_b; ++t) a.flags |= (uint32_t)(p.tokens[first + t] == v) << t;
+        }
+      }
+      const int entry = biased ? s_bias[o] : 0;
+      if (entry) {
+        a.flags |= kBias;
+        a.bias = p.bias_values[q.bias0 + entry - 1];
+      }
+      return a;
+    };
+    Entry first_entry, second_entry;
+    if (listed > 0) first_entry = entry_at(lane);
+    if (listed > 32) second_entry = entry_at(32 + lane);
+
+    // --- a row of a block -----------------------------------------------------
+    auto take_row = [&](const Stage<T>& in, int block, int t) {
+      const int g0 = first_of(block, t), v0 = g0 + lane * 8;
+      const bool closed = (shut >> t) & 1, masked = words_of(t) != nullptr;
+      float* out = kOut ? p.out + (first + t) * p.out_stride : nullptr;
+      auto special_value = [&](const Entry& a, int i) {
+        float w = widen(reinterpret_cast<const T*>(in.raw)[i]);
+        const uint32_t word = masked ? in.mask[(i + (g0 & 31)) >> 5] : kAll;
+        if (q.penal) {
+          const int count = a.count + __popc(a.flags & ((2u << t) - 1));
+          const bool seen = count > 0 || (a.flags & kPrompt);
+          const float p1 = __fdiv_rn(w, q.r), p2 = __fmul_rn(w, q.r);
+          w = seen ? (w > 0.f ? p1 : p2) : w;
+          w = __fsub_rn(w, __fmul_rn(q.freq, (float)count));
+          w = count > 0 ? __fsub_rn(w, q.pres) : w;
+        }
+        w = a.flags & kBias ? __fadd_rn(w, a.bias) : w;
+        return !closed && (word >> ((i + g0) & 31)) & 1 ? w : -INFINITY;
+      };
+      // a lane's first special token
+      uint32_t key = 0;
+      int at = 0;
+      float w0 = 0.f;
+      bool mine = false;
+      if (listed > 0) {
+        const int i = first_entry.v - g0;
+        mine = i >= 0 && i < S::kBlock;
+        w0 = special_value(first_entry, mine ? i : 0);
+        key = mine && w0 > -INFINITY ? ordered(w0) : 0;        // a NaN is no candidate
+        at = first_entry.v;
+      }
+      // the largest value of the tokens that are not special
+      Octet<T> raw[N];
       uint32_t m = Octet<T>::kNone;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const uint32_t open = closed ? 0 : x.bits(n, v0);
+        raw[n] = in.raw[n * 32 + lane];
+        const uint32_t open = closed ? 0 : in.template open<kAligned>(v0 + n * 256, g0, V, masked);
         const uint32_t spec = special ? special_bits(n, v0) : 0;
         if constexpr (kOut) {
-          // special tokens keep their logit: in place, more than 32 are read again
           const int v = v0 + n * 256;
-          float* o = p.out + (first + t) * p.out_stride + v;
           float z[8];
-          x.raw[n].unpack(z);
+          raw[n].unpack(z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = ((open | spec) >> i) & 1 ? z[i] : -INFINITY;
-          if (v >= 0 && v <= V - 8 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-            *reinterpret_cast<float4*>(o) = make_float4(z[0], z[1], z[2], z[3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(z[4], z[5], z[6], z[7]);
+          for (int i = 0; i < 8; ++i) z[i] = (open >> i) & 1 ? z[i] : -INFINITY;
+          if (v >= 0 && v <= V - 8 && (reinterpret_cast<uintptr_t>(out + v) & 15) == 0) {
+            *reinterpret_cast<float4*>(out + v) = make_float4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<float4*>(out + v + 4) = make_float4(z[4], z[5], z[6], z[7]);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (v + i >= 0 && v + i < V) o[i] = z[i];
+              if (v + i >= 0 && v + i < V) out[v + i] = z[i];
           }
         }
-        x.raw[n].drop(open & ~spec);
-        m = x.raw[n].max(m);
+        raw[n].drop(open & ~spec);
+        m = raw[n].max(m);
       }
-      const uint32_t key = ordered(Octet<T>::value(m)), top = __reduce_max_sync(kAll, key);
-      // an equal value of an earlier segment has the lower index
+      const uint32_t dense = ordered(Octet<T>::value(m));
+      if constexpr (kOut) {
+        if (listed > 0) __syncwarp();            // the special ones' places are written
+        if (mine) out[first_entry.v] = w0;
+      }
+      // the rest of them; a lane's tokens ascend
+      for (int e0 = 32; e0 < listed; e0 += 32) {
+        const Entry a = e0 == 32 ? second_entry : entry_at(e0 + lane);
+        const int i = a.v - g0;
+        if (i < 0 || i >= S::kBlock) continue;   // of another block
+        const float w = special_value(a, i);
+        if constexpr (kOut) out[a.v] = w;
+        const uint32_t k = w > -INFINITY ? ordered(w) : 0;
+        if (k > key) {
+          key = k;
+          at = a.v;
+        }
+      }
+      const uint32_t top = __reduce_max_sync(kAll, max(dense, key));
+      // an equal value of an earlier block has the lower index
       const uint32_t held = __shfl_sync(kAll, (uint32_t)(best >> 32), t);
       if (top <= ordered(-INFINITY) || top <= held) return;
       // its place: every lane that has it shows its values to the warp
-      uint32_t at = UINT_MAX;
-      for (uint32_t has = __ballot_sync(kAll, key == top); has; has &= has - 1) {
+      uint32_t place = listed > 0 ? __reduce_min_sync(kAll, key == top ? (uint32_t)at : UINT_MAX) : UINT_MAX;
+      for (uint32_t has = __ballot_sync(kAll, dense == top); has; has &= has - 1) {
         const int who = __ffs(has) - 1;
         __syncwarp();
         if (lane == who) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) sm.stage[n] = x.raw[n];
+          for (int n = 0; n < N; ++n) sm.top[n] = raw[n];
         }
         __syncwarp();
-        const bool in = lane < N * 8;
-        const float z = in ? widen(reinterpret_cast<const T*>(sm.stage)[lane]) : -INFINITY;
-        const int i = __ffs(__ballot_sync(kAll, in && ordered(z) == top)) - 1;
-        at = min(at, (uint32_t)(v0 + (who - lane) * 8 + i / 8 * 256 + i % 8));
+        const bool in_top = lane < N * 8;
+        const float z = in_top ? widen(reinterpret_cast<const T*>(sm.top)[lane]) : -INFINITY;
+        const int i = __ffs(__ballot_sync(kAll, in_top && ordered(z) == top)) - 1;
+        place = min(place, (uint32_t)(v0 + (who - lane) * 8 + i / 8 * 256 + i % 8));
       }
-      if (lane == t) best = ((unsigned long long)top << 32) | (uint32_t)~at;
+      if (lane == t) best = ((unsigned long long)top << 32) | (uint32_t)~place;
     };
-    for (int e0 = 0; e0 == 0 || e0 < listed; e0 += 32) {
-      if (listed > 0) load_special(e0 + lane);
-      if (e0 == 0) {
-        const int block1 = (seg + 1) * S::kBlocks;
-        for (int block = seg * S::kBlocks; block < block1; ++block) {
-          for (int t = 0; t < T_b; ++t) {
-            Vecs now = x;
-            const bool more = t + 1 < T_b;       // or else the next block's first row
-            if (more || block + 1 < seg1 * S::kBlocks) load_row(more ? block : block + 1, more ? t + 1 : 0);
-            if (!more && block + 1 == block1 && q.penal && seg + 1 < seg1) load_state(seg + 1);
-            take_row(now, block, t);
-          }
-        }
-        if constexpr (kOut) __syncwarp();        // the special ones' places are written
-      }
-      if (listed == 0) break;
-      // --- the special tokens ----------------------------------------------------
-      const bool live = e0 + lane < listed, in_prompt = sp.held < 0;
-      const bool in_block = live && (sm.block[sp.o >> 5] >> (sp.o & 31)) & 1;
-      int count = sp.held & 0x7fff;
-      if (in_block)
-        for (int s = 0; s < skip; ++s) count += p.tokens[q.first + s] == sp.v;
-      uint32_t key[kChunk];
-#pragma unroll
-      for (int t = 0; t < kChunk; ++t) {
-        key[t] = 0;
-        if (t >= T_b) break;
-        if (in_block) count += p.tokens[first + t] == sp.v;
-        float w = widen(sp.z[t]);
-        if (q.penal) {
-          if (count > 0 || in_prompt) w = w > 0.f ? __fdiv_rn(w, q.r) : __fmul_rn(w, q.r);
-          w = __fsub_rn(w, __fmul_rn(q.freq, (float)count));
-          if (count > 0) w = __fsub_rn(w, q.pres);
-        }
-        if (sp.entry) w = __fadd_rn(w, sp.bias);
-        if (!((sp.word[t] >> (sp.v & 31)) & 1) || (shut >> t) & 1) w = -INFINITY;
-        if constexpr (kOut) {
-          const int from = lo - shift_of(t);
-          if (live && (kAligned || (sp.v >= from && sp.v < from + S::kTokens)))
-            p.out[(first + t) * p.out_stride + sp.v] = w;
-        }
-        if (w > -INFINITY) key[t] = ordered(w);  // a NaN is no candidate
-      }
-      // the warp's best of each row, to the lane that keeps it; no branch between,
-      // so that the rows' reductions overlap
-      uint32_t top = 0, at = 0;
-#pragma unroll
-      for (int t = 0; t < kChunk; ++t) {
-        if (t >= T_b) break;
-        const uint32_t m = __reduce_max_sync(kAll, key[t]);
-        const uint32_t v = __reduce_min_sync(kAll, key[t] == m ? (uint32_t)sp.v : UINT_MAX);
-        if (lane == t) {
-          top = m;
-          at = v;
-        }
-      }
-      if (top > 0) {
-        const unsigned long long c = ((unsigned long long)top << 32) | (uint32_t)~at;
-        if (c > best) best = c;
+    const int block1 = (seg + 1) * S::kBlocks;
+    for (int block = seg * S::kBlocks; block < block1; ++block) {
+      for (int t = 0; t < T_b; ++t) {
+        copies_wait<kStages - 2>();
+        __syncwarp();                            // every lane's copies, and the last row read
+        copy_next();
+        if (t + 1 == T_b && block + 1 == block1 && q.penal && seg + 1 < seg1) load_state(seg + 1);
+        take_row(sm.ring[stage], block, t);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
       }
     }
+    __syncwarp();
     if (biased)                                  // clean for the next segment
       for (int e = lane; e < listed; e += 32) s_bias[sm.list[e]] = 0;
     __syncwarp();
