@@ -19,7 +19,7 @@
 // instructions and latency: a step's rows are few, and everything before the
 // logits (offsets, state, biases, masks) is a chain of loads. So a warp works for
 // itself, without block barriers: it takes a run of segments of the vocabulary
-// (1024 tokens) for up to kChunk rows of a sequence. Of a segment only few tokens
+// (1024 tokens) for up to 8 rows of a sequence. Of a segment only few tokens
 // are touched by a penalty or a bias ("special"). It marks them in a bitmap, lists
 // them and fetches what they need, a token a lane. Then, a row of a block after the
 // other, with the next one's logits and mask on their way to shared memory:
@@ -34,14 +34,13 @@
 // its runs.
 //
 // Measured, 16 x 16 rows of 131072 bf16 logits with 2.6% of special tokens and
-// half of the rows masked (73 MB): 32 us (2.3 TB/s); without biases and masks 26 us;
-// without penalties too 20 us (3.4 TB/s). 426 rows of 100003 fp32 with masks and
-// output (359 MB): 78 us (4.6 TB/s), as bf16 without output 45 us. The rows in
-// registers, one ahead, and the special tokens of the chunk's rows together from
-// global memory: 34, 29, 18, 81 and 50 us. Three stages 34 and 78 us; 20 warps to an
-// SM (96 registers) 32 and 80 us. A CTA to a window of 4096 or 8192 tokens with block
-// barriers 33 and 82 us; dense and special CTAs side by side 33 and 147; rows in
-// chunks of 8 33 and 95 (long and short blocks do not end together).
+// half of the rows masked (73 MB): 27 us (2.7 TB/s); without penalties, biases and
+// masks 18 us (3.7 TB/s). 426 rows of 100003 fp32 with masks and output (359 MB): 79
+// us (4.5 TB/s), as bf16 without output 41 us. 4 rows to a warp: 32, 20, 78 and 45 us.
+// Those 4 in registers, one ahead, and their special tokens together from global
+// memory: 34, 18, 81 and 50 us. With 4 rows, 3 stages 34 and 78 us, 20 warps to an SM
+// (96 registers) 32 and 80 us. A CTA to a window of 4096 or 8192 tokens with block
+// barriers 33 and 82 us; dense and special CTAs side by side 33 and 147.
 //
 // Rows of an odd vocabulary start at any alignment. Each row's vector grid is
 // shifted to its own 16-byte boundary and its segments with it, so the loads stay
@@ -60,9 +59,10 @@ namespace {
 
 constexpr int kThreads = 256;        // of the history kernels
 constexpr int kMaxBlock = 128;       // verify rows of a sequence
-// Rows of a warp: enough to share a segment's set-up, few enough that sequences
-// of long and short blocks end together and that few sequences fill the GPU.
-constexpr int kChunk = 4;
+// Most rows of a warp: enough to share a segment's set-up, few enough that sequences
+// of long and short blocks end together (16: 26 us instead of 27 for 16 x 16 rows, 91
+// instead of 78 for the ragged fp32 batch).
+constexpr int kChunkMost = 8;
 constexpr int kWarpsPerCta = 4;
 // Warps beyond which segments are taken in turn, for each SM
 constexpr long long kWarpsPerSm = 64;
@@ -97,7 +97,8 @@ struct TargetParams {
   int segments;                      // of a row
   int span;                          // segments of a run
   int runs;
-  int chunks;                        // of kChunk rows, to max_block
+  int chunk;                         // rows of a warp
+  int chunks;                        // to max_block
   int* status;
 };
 
@@ -337,7 +338,7 @@ template <typename T>
 struct WarpSmem {
   uint32_t map[Segment<T>::kWords + 1];    // special tokens
   uint32_t block[Segment<T>::kWords + 1];  // those of the block among them
-  const uint32_t* words[kChunk];           // of the rows' masks, nullptr for none
+  const uint32_t* words[kChunkMost];       // of the rows' masks, nullptr for none
   uint16_t list[Segment<T>::kBits];
   alignas(16) Octet<T> top[Segment<T>::kOctets]; // a lane's octets that have a maximum
   Stage<T> ring[kStages];
@@ -361,10 +362,10 @@ choose_kernel(TargetParams p) {
   const unsigned unit = work / p.runs;
   const int chunk = unit % p.chunks, b = unit / p.chunks;
   if (b >= p.num_seqs) return;
-  const int skip = chunk * kChunk;               // rows before this chunk
+  const int skip = chunk * p.chunk;              // rows before this chunk
   const bool lead = chunk == 0 && run == 0 && lane == 0;
   const SeqParams q(p, b, lead);
-  const int T_b = min(q.T - skip, kChunk), first = q.first + skip;
+  const int T_b = min(q.T - skip, p.chunk), first = q.first + skip;
   if (T_b <= 0) return;
   const int V = p.vocab;
   const bool biased = q.bias1 > q.bias0, special = q.special();
@@ -483,7 +484,7 @@ choose_kernel(TargetParams p) {
       float bias;
       uint32_t flags;                            // bit t: row t's token is v
     };
-    constexpr uint32_t kPrompt = 1u << kChunk, kBias = 2u << kChunk;
+    constexpr uint32_t kPrompt = 1u << kChunkMost, kBias = 2u << kChunkMost;
     auto entry_at = [&](int e) {
       Entry a{INT_MIN / 4, 0, 0.f, 0};
       const int o = e < listed ? sm.list[e] : 0, v = base + o;
@@ -831,14 +832,22 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
   const int sms = device_sm_count();
   if (sms <= 0) return SPLASH_ERR_CUDA;
 
-  // A warp for each segment while that does not fill the GPU, then longer runs: a
-  // run's first loads and last merge are shared by more tokens. Chunks count only
-  // as far as there are rows.
   const bool aligned = aligned16(logits) && logits_stride * es % 16 == 0;
-  const int chunks = (max_block_len + kChunk - 1) / kChunk;
-  const long long full = num_seqs + (long long)num_rows / kChunk;
-  const long long units = num_seqs * (long long)chunks < full ? num_seqs * (long long)chunks : full;
   const long long segments = segments_for(vocab, dtype, aligned);
+  // Fewer rows to a warp where 8 would leave a quarter of the GPU's warps (16 to an
+  // SM) without work: 16 x 16 rows of 32000 logits 21 us at 8, 15 at 4, 17 at 2.
+  // Chunks count only as far as there are rows.
+  int chunk = kChunkMost;
+  long long units = 0;
+  for (;; chunk /= 2) {
+    const long long by_block = num_seqs * (long long)((max_block_len + chunk - 1) / chunk);
+    const long long by_rows = num_seqs + (long long)num_rows / chunk;
+    units = by_block < by_rows ? by_block : by_rows;
+    if (chunk == 1 || units * segments >= 12LL * sms) break;
+  }
+  const int chunks = (max_block_len + chunk - 1) / chunk;
+  // A warp for each segment while that does not fill the GPU, then longer runs: a
+  // run's first loads and last merge are shared by more tokens.
   long long span = units * segments / (kWarpsPerSm * sms);
   span = span < 1 ? 1 : span;
   const long long runs = (segments + span - 1) / span;
@@ -850,7 +859,7 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
                  frequency, num_bias > 0 ? bias_offsets : nullptr, bias_ids, bias_values, num_bias,
                  mask, mask_stride, mask_rows, num_masks, out, out_stride, target_tokens,
                  static_cast<unsigned long long*>(workspace), (int)segments, (int)span, (int)runs,
-                 chunks, device_status};
+                 chunk, chunks, device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = dtype == SPLASH_F32    ? launch_choose<float>(p, aligned, s)
                   : dtype == SPLASH_BF16 ? launch_choose<__nv_bfloat16>(p, aligned, s)
