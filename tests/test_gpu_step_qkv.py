@@ -402,3 +402,28 @@ def test_rows_further_apart_than_32_bits():
     want, wpool, _ = run(q, k, v, slots, pages, pos, inv_freq=f)
     got, gpool, _ = run(row[:, :4], row[:, 4:5], row[:, 5:], slots, pages, pos, inv_freq=f)
     assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(gpool, wpool))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,hq,hkv", [(3, 20, 6), (700, 24, 4), (2431, 3, 1), (5003, 5, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_a_token_comes_out_the_same_in_a_call_of_many_and_of_few(n, hq, hkv, D, dtype):
+    """A warp's tokens, with skipped ones between, against calls of 1 to 40 tokens,
+    where every batch of a token has a warp of its own."""
+    q, k, v, slots, pages = make(n + hq, n, hq, hkv, D, dtype)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    slots[torch.rand(n, generator=g, device="cuda") < 0.4] = -1
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, device="cuda", dtype=torch.int32)
+    f = torch.rand(D // 2, generator=g, device="cuda")
+    w = torch.rand(D, generator=g, device="cuda") + 0.5
+    a = dict(inv_freq=f, q_weight=w, k_weight=w)
+    want, wpool, st = run(q, k, v, slots, pages, pos, **a)
+    got, gpool = torch.full_like(want, 99.0), pool_of(pages, hkv, D)
+    at = 0
+    while at < n:
+        m = min(n - at, 1 + at % 40)
+        part = slice(at, at + m)
+        sk.splash_qkv_append(q[part], k[part], v[part], got[part], *gpool, pos[part], slots[part], **a)
+        at += m
+    assert st == 0 and torch.equal(got, want)
+    assert all(torch.equal(x, y) for x, y in zip(gpool, wpool))
