@@ -23,24 +23,24 @@
 // are touched by a penalty or a bias ("special"). It marks them in a bitmap, lists
 // them and fetches what they need, a token a lane. Then, a row of a block after the
 // other, with the next one's logits and mask on their way to shared memory:
-//   - it takes the maximum of the logits as they are stored: excluded tokens
-//     (special ones, and those that the mask closes) become -inf by one logic
-//     operation a register, and 16-bit types stay packed in pairs;
-//   - it computes the special tokens exactly, from the copy in shared memory;
-//   - the place of the larger of both is looked up only where it beats the run's
-//     best.
+//   - it computes the special tokens exactly and puts them back in the copy (-inf
+//     and a key beside it where the logits have 16 bits);
+//   - it takes the maximum of the row as it is stored: what the mask closes becomes
+//     -inf by one logic operation a register, and 16-bit types stay packed in pairs;
+//   - the place of the maximum is looked up only where it beats the run's best.
 // Choices are 64-bit keys (ordered value, complement of the index) merged by
 // maximum, which no order changes; a second kernel takes each row's maximum over
 // its runs.
 //
 // Measured, 16 x 16 rows of 131072 bf16 logits with 2.6% of special tokens and
 // half of the rows masked (73 MB): 27 us (2.7 TB/s); without penalties, biases and
-// masks 18 us (3.7 TB/s). 426 rows of 100003 fp32 with masks and output (359 MB): 79
-// us (4.5 TB/s), as bf16 without output 41 us. 4 rows to a warp: 32, 20, 78 and 45 us.
-// Those 4 in registers, one ahead, and their special tokens together from global
-// memory: 34, 18, 81 and 50 us. With 4 rows, 3 stages 34 and 78 us, 20 warps to an SM
-// (96 registers) 32 and 80 us. A CTA to a window of 4096 or 8192 tokens with block
-// barriers 33 and 82 us; dense and special CTAs side by side 33 and 147.
+// masks 16.6 us (4.0 TB/s). 426 rows of 100003 fp32 with masks and output (359 MB): 73
+// us (4.9 TB/s), as bf16 without output 41 us. 16 warps to an SM instead of 20: 27, 16,
+// 76 and 45 us; 24: 28, 17, 81 and 49 us. Earlier forms: special tokens kept out of the
+// dense pass by their bitmap 27, 18, 79 and 41 us; that with 4 rows to a warp 32, 20,
+// 78 and 45 us; those 4 in registers, one ahead, and their special tokens together
+// from global memory 34, 18, 81 and 50 us. A CTA to a window of 4096 or 8192 tokens
+// with block barriers 33 and 82 us; dense and special CTAs side by side 33 and 147.
 //
 // Rows of an odd vocabulary start at any alignment. Each row's vector grid is
 // shifted to its own 16-byte boundary and its segments with it, so the loads stay
@@ -64,6 +64,7 @@ constexpr int kMaxBlock = 128;       // verify rows of a sequence
 // instead of 78 for the ragged fp32 batch).
 constexpr int kChunkMost = 8;
 constexpr int kWarpsPerCta = 4;
+constexpr int kWarpsResident = 20;   // to an SM: 96 registers a thread, 44 KB to a CTA
 // Warps beyond which segments are taken in turn, for each SM
 constexpr long long kWarpsPerSm = 64;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -315,7 +316,11 @@ struct Stage {
       }
     }
   }
-  // The bits of octet n, token v on, that are in the row and open in its mask
+  template <bool kAligned>
+  __device__ bool at_end(int g0, int V) const {
+    return (!kAligned && g0 < 0) || g0 + Segment<T>::kBlock > V;
+  }
+  // The bits of the 8 tokens from v on that are in the row and open in its mask
   // (upper bits: others').
   template <bool kAligned>
   __device__ uint32_t open(int v, int g0, int V, bool masked) const {
@@ -324,7 +329,7 @@ struct Stage {
       const int i = (v >> 5) - (g0 >> 5);
       on = kAligned ? mask[i] >> (v & 31) : __funnelshift_r(mask[i], mask[i + 1], v & 31);
     }
-    if ((!kAligned && g0 < 0) || g0 + Segment<T>::kBlock > V) {
+    if (at_end<kAligned>(g0, V)) {
       const int from = v < 0 ? -v : 0, to = V - v < 8 ? V - v : 8;
       on &= to > 0 && from < 8 ? ((1u << to) - 1) & ~((1u << from) - 1) : 0;
     }
@@ -340,12 +345,11 @@ struct WarpSmem {
   uint32_t block[Segment<T>::kWords + 1];  // those of the block among them
   const uint32_t* words[kChunkMost];       // of the rows' masks, nullptr for none
   uint16_t list[Segment<T>::kBits];
-  alignas(16) Octet<T> top[Segment<T>::kOctets]; // a lane's octets that have a maximum
   Stage<T> ring[kStages];
 };
 
 template <typename T, bool kOut, bool kAligned>
-__global__ void __launch_bounds__(32 * kWarpsPerCta, 16 / kWarpsPerCta)
+__global__ void __launch_bounds__(32 * kWarpsPerCta, kWarpsResident / kWarpsPerCta)
 choose_kernel(TargetParams p) {
   using S = Segment<T>;
   constexpr int N = S::kOctets;
@@ -511,13 +515,25 @@ choose_kernel(TargetParams p) {
     if (listed > 32) second_entry = entry_at(32 + lane);
 
     // --- a row of a block -----------------------------------------------------
-    auto take_row = [&](const Stage<T>& in, int block, int t) {
+    auto take_row = [&](Stage<T>& in, int block, int t) {
+      constexpr bool kExact = sizeof(T) == 4;    // a processed logit has the logits' type
       const int g0 = first_of(block, t), v0 = g0 + lane * 8;
       const bool closed = (shut >> t) & 1, masked = words_of(t) != nullptr;
+      const bool whole = !closed && !masked && !in.template at_end<kAligned>(g0, V);
       float* out = kOut ? p.out + (first + t) * p.out_stride : nullptr;
-      auto special_value = [&](const Entry& a, int i) {
-        float w = widen(reinterpret_cast<const T*>(in.raw)[i]);
-        const uint32_t word = masked ? in.mask[(i + (g0 & 31)) >> 5] : kAll;
+      T* values = reinterpret_cast<T*>(in.raw);
+      // The special tokens, a lane's in ascending order. Their processed logits take
+      // the logits' place; where those have fewer bits, -inf does, and the largest
+      // of a lane's is kept beside it.
+      // In the output of such a type a place is written after the dense pass; the
+      // ones past 64 stay in that case and are done then.
+      constexpr bool kLate = kOut && !kExact;
+      uint32_t key = 0;
+      int at = 0;
+      auto special_token = [&](const Entry& a) {
+        const int i = a.v - g0;
+        if (i < 0 || i >= S::kBlock) return 0.f; // of another block
+        float w = widen(values[i]);
         if (q.penal) {
           const int count = a.count + __popc(a.flags & ((2u << t) - 1));
           const bool seen = count > 0 || (a.flags & kPrompt);
@@ -527,34 +543,38 @@ choose_kernel(TargetParams p) {
           w = count > 0 ? __fsub_rn(w, q.pres) : w;
         }
         w = a.flags & kBias ? __fadd_rn(w, a.bias) : w;
-        return !closed && (word >> ((i + g0) & 31)) & 1 ? w : -INFINITY;
+        if constexpr (kExact) {
+          values[i] = w;
+        } else {
+          if (!whole && (closed || !(in.template open<kAligned>(a.v, g0, V, masked) & 1))) w = -INFINITY;
+          reinterpret_cast<uint16_t*>(values)[i] = (uint16_t)Octet<T>::kNone;
+          const uint32_t k = w > -INFINITY ? ordered(w) : 0;     // a NaN is no candidate
+          if (k > key) {
+            key = k;
+            at = a.v;
+          }
+        }
+        return w;
       };
-      // a lane's first special token
-      uint32_t key = 0;
-      int at = 0;
-      float w0 = 0.f;
-      bool mine = false;
+      float first_w = 0.f, second_w = 0.f;
       if (listed > 0) {
-        const int i = first_entry.v - g0;
-        mine = i >= 0 && i < S::kBlock;
-        w0 = special_value(first_entry, mine ? i : 0);
-        key = mine && w0 > -INFINITY ? ordered(w0) : 0;        // a NaN is no candidate
-        at = first_entry.v;
+        first_w = special_token(first_entry);
+        if (listed > 32) second_w = special_token(second_entry);
+        if constexpr (!kLate)
+          for (int e0 = 64; e0 < listed; e0 += 32) special_token(entry_at(e0 + lane));
+        __syncwarp();
       }
-      // the largest value of the tokens that are not special
-      Octet<T> raw[N];
+      const bool late = kLate && listed > 64;
+      // the largest of the open ones
       uint32_t m = Octet<T>::kNone;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        raw[n] = in.raw[n * 32 + lane];
-        const uint32_t open = closed ? 0 : in.template open<kAligned>(v0 + n * 256, g0, V, masked);
-        const uint32_t spec = special ? special_bits(n, v0) : 0;
+        const int v = v0 + n * 256;
+        Octet<T> raw = in.raw[n * 32 + lane];
+        if (!whole) raw.drop(closed ? 0 : in.template open<kAligned>(v, g0, V, masked));
         if constexpr (kOut) {
-          const int v = v0 + n * 256;
           float z[8];
-          raw[n].unpack(z);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = (open >> i) & 1 ? z[i] : -INFINITY;
+          raw.unpack(z);
           if (v >= 0 && v <= V - 8 && (reinterpret_cast<uintptr_t>(out + v) & 15) == 0) {
             *reinterpret_cast<float4*>(out + v) = make_float4(z[0], z[1], z[2], z[3]);
             *reinterpret_cast<float4*>(out + v + 4) = make_float4(z[4], z[5], z[6], z[7]);
@@ -564,45 +584,36 @@ choose_kernel(TargetParams p) {
               if (v + i >= 0 && v + i < V) out[v + i] = z[i];
           }
         }
-        raw[n].drop(open & ~spec);
-        m = raw[n].max(m);
+        if (late) raw.drop(~special_bits(n, v0));
+        m = raw.max(m);
       }
       const uint32_t dense = ordered(Octet<T>::value(m));
-      if constexpr (kOut) {
-        if (listed > 0) __syncwarp();            // the special ones' places are written
-        if (mine) out[first_entry.v] = w0;
-      }
-      // the rest of them; a lane's tokens ascend
-      for (int e0 = 32; e0 < listed; e0 += 32) {
-        const Entry a = e0 == 32 ? second_entry : entry_at(e0 + lane);
-        const int i = a.v - g0;
-        if (i < 0 || i >= S::kBlock) continue;   // of another block
-        const float w = special_value(a, i);
-        if constexpr (kOut) out[a.v] = w;
-        const uint32_t k = w > -INFINITY ? ordered(w) : 0;
-        if (k > key) {
-          key = k;
-          at = a.v;
+      if constexpr (kLate) {
+        if (listed > 0) __syncwarp();            // the dense pass has written
+        auto write = [&](int v, float w) {
+          if (v >= g0 && v < g0 + S::kBlock) out[v] = w;
+        };
+        if (listed > 0) write(first_entry.v, first_w);
+        if (listed > 32) write(second_entry.v, second_w);
+        for (int e0 = 64; e0 < listed; e0 += 32) {
+          const Entry a = entry_at(e0 + lane);
+          write(a.v, special_token(a));
         }
+        if (late) __syncwarp();                  // no special token has a value now
       }
       const uint32_t top = __reduce_max_sync(kAll, max(dense, key));
       // an equal value of an earlier block has the lower index
       const uint32_t held = __shfl_sync(kAll, (uint32_t)(best >> 32), t);
       if (top <= ordered(-INFINITY) || top <= held) return;
-      // its place: every lane that has it shows its values to the warp
-      uint32_t place = listed > 0 ? __reduce_min_sync(kAll, key == top ? (uint32_t)at : UINT_MAX) : UINT_MAX;
+      // its place: the warp looks through the values of every lane that has it
+      uint32_t place = UINT_MAX;
+      if (!kExact && listed > 0) place = __reduce_min_sync(kAll, key == top ? (uint32_t)at : UINT_MAX);
       for (uint32_t has = __ballot_sync(kAll, dense == top); has; has &= has - 1) {
-        const int who = __ffs(has) - 1;
-        __syncwarp();
-        if (lane == who) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) sm.top[n] = raw[n];
-        }
-        __syncwarp();
-        const bool in_top = lane < N * 8;
-        const float z = in_top ? widen(reinterpret_cast<const T*>(sm.top)[lane]) : -INFINITY;
-        const int i = __ffs(__ballot_sync(kAll, in_top && ordered(z) == top)) - 1;
-        place = min(place, (uint32_t)(v0 + (who - lane) * 8 + i / 8 * 256 + i % 8));
+        const int i = (lane / 8 * 32 + __ffs(has) - 1) * 8 + lane % 8;
+        bool found = lane < N * 8 && ordered(widen(values[lane < N * 8 ? i : 0])) == top;
+        if (!whole) found = found && (in.template open<kAligned>(g0 + i, g0, V, masked) & 1);
+        const uint32_t where = __ballot_sync(kAll, found);
+        place = min(place, (uint32_t)__shfl_sync(kAll, g0 + i, __ffs(where) - 1));
       }
       if (lane == t) best = ((unsigned long long)top << 32) | (uint32_t)~place;
     };
@@ -854,8 +865,9 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
 
   const bool aligned = aligned16(logits) && logits_stride * es % 16 == 0;
   const long long segments = segments_for(vocab, dtype, aligned);
-  // Fewer rows to a warp where 8 would leave a quarter of the GPU's warps (16 to an
-  // SM) without work: 16 x 16 rows of 32000 logits 21 us at 8, 15 at 4, 17 at 2.
+  // Fewer rows to a warp where 8 would leave more than a third of the GPU's warps
+  // (20 to an SM) without work: 16 x 16 rows of 32000 logits 21 us at 8, 16 at 4, 18
+  // at 2.
   // Chunks count only as far as there are rows.
   int chunk = kChunkMost;
   long long units = 0;
