@@ -296,7 +296,14 @@ qkv_append_kernel(QkvParams p) {
     const int page = slot / kPageSize, at = slot % kPageSize;
     if (slot < 0 || page >= p.num_pages) {       // a padded row: nothing is written
       if (slot >= 0 && lane == 0) report(p.status, SPLASH_DEVICE_BAD_PAGE);
-      for (int bi = b0; bi < b1; ++bi) {
+      // its batches that are on their way are dropped, no more of them read
+      int copied = b1 - b0;
+      if (next == item) {
+        copied = next_b - b0;
+        next += step;
+        next_item();
+      }
+      for (; copied > 0; --copied) {
         copies_wait<kStages - 2>();
         copy_next();
         stage = stage == kStages - 1 ? 0 : stage + 1;
