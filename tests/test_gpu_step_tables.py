@@ -241,3 +241,26 @@ def test_misaligned_outputs():
     torch.cuda.synchronize()
     assert np.array_equal(pos.cpu().numpy(), want[5]) and np.array_equal(slots.cpu().numpy(), want[6])
     assert flat[0].item() == -9 and set(flat[n + 1:n + 3].tolist()) == {-9}
+
+
+@pytest.mark.parametrize("ctx0", [0, 1, 15, 16, 37])
+def test_bad_pages_inside_long_blocks(ctx0):
+    """Blocks of thousands of rows from any offset in a page, held pages and pages
+    of the free list out of the pool among theirs."""
+    ctx, T = np.array([ctx0, 5, ctx0 + 3]), np.array([3001, 1, 5200])
+    held = np.array([120, 1, 200])
+    total, width = 900, 400
+    r = np.random.default_rng(ctx0)
+    ids = r.permutation(total)
+    table = np.full((3, width), -1)
+    at = 0
+    for b in range(3):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    free = ids[at:].copy()
+    table[0, 7], table[2, 199], table[2, 0] = total, -3, total + 5
+    free[-9], free[-40] = -1, total
+    n = int(T.sum()) + 5
+    want = S.build_tables(ctx, T, table, held, free, len(free), n, total)
+    assert want[-1] == {S.BAD_PAGE}
+    check(build(ctx, T, table, held, free, len(free), n, total)[0], want)
