@@ -419,7 +419,7 @@ choose_kernel(TargetParams p) {
   for (int seg = seg0; seg < seg1; ++seg) {
     const int lo = seg * S::kTokens, base = lo - 32;        // first token of bitmap bit 0
     const int wlo = max(0, lo - S::kEarly), whi = min(V, lo + S::kTokens);
-    int listed = 0;
+    int listed = 0, below = 0;                   // below: before the second block's tokens
     auto special_bits = [&](int n, int v0) -> uint32_t {
       const uint32_t* w = sm.map + ((v0 - base) >> 5) + n * 8;
       return kAligned ? w[0] >> (v0 & 31) : __funnelshift_r(w[0], w[1], v0 & 31);
@@ -476,6 +476,7 @@ choose_kernel(TargetParams p) {
       }
       listed = __shfl_sync(kAll, at, 31);
       at -= mine;
+      below = __shfl_sync(kAll, at, 16);         // lane 16: tokens from lo + 512 on
       for (uint32_t w = before; w; w &= w - 1) sm.list[at++] = (uint16_t)(__ffs(w) - 1);
       for (; m; m &= m - 1) sm.list[at++] = (uint16_t)(lane * 32 + 31 + __ffs(m));
       __syncwarp();
@@ -560,8 +561,14 @@ choose_kernel(TargetParams p) {
       if (listed > 0) {
         first_w = special_token(first_entry);
         if (listed > 32) second_w = special_token(second_entry);
-        if constexpr (!kLate)
-          for (int e0 = 64; e0 < listed; e0 += 32) special_token(entry_at(e0 + lane));
+        if constexpr (!kLate) {
+          // those of this block; a shifted row's second one begins a little earlier
+          static_assert(S::kBlocks == 1 || S::kBlock == 512, "lane 16");
+          const bool second = block % S::kBlocks != 0;
+          const int e1 = S::kBlocks == 1 || second ? listed : below;
+          for (int e0 = second ? max((below - S::kEarly) & ~31, 64) : 64; e0 < e1; e0 += 32)
+            special_token(entry_at(e0 + lane));
+        }
         __syncwarp();
       }
       const bool late = kLate && listed > 64;
