@@ -431,11 +431,12 @@ int splash_verify_attention_fixed_scratch(const uint16_t* q, int num_q_tokens,
  *     page * P + position % P of row q_offsets[b] + t. Rows without a slot (of
  *     a sequence that is not served or whose lengths are out of range, and the
  *     rows past the last sequence of a padded batch) get slot -1, position 0.
- * A length out of range or a sequence whose rows pass num_tokens reports
- * SPLASH_DEVICE_BAD_LENGTH, gets no pages and no slots; the others keep their
- * rows. A page id outside [0, num_pages) reports SPLASH_DEVICE_BAD_PAGE and
- * maps no slot. *free_count is cut to [0, free_capacity]. num_pages * P must
- * fit 32 bits. Page numbers only: no pool is touched.
+ * A length or page count out of range or a sequence whose rows pass num_tokens
+ * reports SPLASH_DEVICE_BAD_LENGTH, gets no pages and no slots and keeps its page
+ * count; the others keep their rows. A page id outside [0, num_pages) reports
+ * SPLASH_DEVICE_BAD_PAGE and maps no slot. *free_count is cut to
+ * [0, free_capacity]. num_pages * P must fit 32 bits. Page numbers only: no pool
+ * is touched.
  */
 int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
                         int num_tokens, int page_size, int num_pages, int32_t* page_table,
@@ -454,10 +455,11 @@ int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, 
  * order. page_counts_out and free_count_out may be their inputs.
  * released_offsets [num_seqs + 1]: exclusive prefix of the pages given back. A
  * sequence whose pages do not fit free_capacity keeps them, and so does every
- * later one that gives some back (SPLASH_DEVICE_BAD_LENGTH). The page table is
- * only read: entries past page_counts_out[b] are stale. A page that sequences
- * share is given back once per sequence that holds it, so shared prefixes stay
- * inside keep_lens of all but one.
+ * later one that gives some back (SPLASH_DEVICE_BAD_LENGTH); one whose page
+ * count is out of range gives back nothing and keeps its count (the same code).
+ * The page table is only read: entries past page_counts_out[b] are stale. A page
+ * that sequences share is given back once per sequence that holds it, so shared
+ * prefixes stay inside keep_lens of all but one.
  */
 int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* page_table,
                          int max_pages_per_seq, int page_size, const int32_t* page_counts,

@@ -37,7 +37,6 @@ def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages)
         bad = t < 0 or c < 0 or c + t > max_pages * PAGE or not 0 <= have <= max_pages
         if bad:
             codes.add(BAD_LENGTH)
-        have = counts[b] = max(0, min(have, max_pages))
         q_off.append(q_off[-1] + rows)
         need = 0 if bad or rows == 0 else max(0, pages_of(c + t) - have)
         asked += need
@@ -56,8 +55,7 @@ def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages)
             codes.add(OUT_OF_PAGES)
         counts[b] += got
         new_off.append(new_off[-1] + got)
-        lengths_ok = t >= 0 and c >= 0 and c + t <= max_pages * PAGE
-        if lengths_ok and fits and pages_of(c + t) <= counts[b]:
+        if not bad and fits and pages_of(c + t) <= counts[b]:
             for i in range(rows):
                 page = int(table[b, (c + i) // PAGE])
                 if not 0 <= page < num_pages:
@@ -78,7 +76,6 @@ def release_pages(keep, table, counts, free, free_count):
         have = counts[b]
         if not 0 <= have <= table.shape[1]:
             codes.add(BAD_LENGTH)
-            counts[b] = max(0, min(have, table.shape[1]))
             off.append(off[-1])
             continue
         left = have if keep[b] < 0 else min(have, pages_of(int(keep[b])))

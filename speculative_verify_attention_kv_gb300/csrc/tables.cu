@@ -132,6 +132,10 @@ __device__ inline bool lengths_bad(int ctx, int T, int max_pages) {
   return T < 0 || ctx < 0 || (long long)ctx + T > (long long)max_pages * kPageSize;
 }
 
+// Such a sequence keeps its count as it is: cut to the table's width it would look
+// like a valid one, whose entries are stale.
+__device__ inline bool count_bad(int pages, int max_pages) { return pages < 0 || pages > max_pages; }
+
 // Table entries and slots; thread `tid` of `threads` over the whole grid.
 // q_off and new_off: the scan's sums [B + 1], in shared or global memory.
 __device__ inline void fill_tables(const TablesParams& p, const int32_t* q_off,
@@ -168,8 +172,8 @@ __device__ inline void fill_tables(const TablesParams& p, const int32_t* q_off,
         const int T = p.T[b], have = p.counts_out[b];
         nfirst = new_off[b];
         held = have - (new_off[b + 1] - nfirst);
-        ok = !lengths_bad(ctx, T, p.max_pages) && (long long)first + T <= p.num_tokens &&
-             pages_of((long long)ctx + T) <= have;
+        ok = !lengths_bad(ctx, T, p.max_pages) && !count_bad(have, p.max_pages) &&
+             (long long)first + T <= p.num_tokens && pages_of((long long)ctx + T) <= have;
       }
       if (!ok) continue;
       const int pos = ctx + (int)(i - first), j = pos / kPageSize;
@@ -214,8 +218,7 @@ __global__ void __launch_bounds__(N) tables_scan_kernel(TablesParams p, int fill
       ctx = p.ctx[b];
       T = p.T[b];
       have = p.counts[b];
-      bad = lengths_bad(ctx, T, p.max_pages) || have < 0 || have > p.max_pages;
-      have = max(0, min(have, p.max_pages));
+      bad = lengths_bad(ctx, T, p.max_pages) || count_bad(have, p.max_pages);
       if (bad) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
       T = max(T, 0);
     }
@@ -305,9 +308,8 @@ __global__ void __launch_bounds__(N) release_scan_kernel(ReleaseParams p, int fi
     int have = 0, left = 0;
     if (b < B) {
       have = p.counts[b];
-      if (have < 0 || have > p.max_pages) {
+      if (count_bad(have, p.max_pages)) {
         report(p.status, SPLASH_DEVICE_BAD_LENGTH);
-        have = max(0, min(have, p.max_pages));
         left = have;                                  // nothing given back
       } else {
         const int keep = p.keep[b];
