@@ -402,7 +402,7 @@ int splash_verify_attention_fixed_scratch(const uint16_t* q, int num_q_tokens,
  * The rest of a verify step. Page tables and slot maps, the projections'
  * norm, rotation and append, and the target's choices, so that a step's
  * lengths, pages and tokens stay on the device:
- *   splash_build_tables -> splash_qkv_append -> splash_verify_attention
+ *   splash_build_tables_served -> splash_qkv_append -> splash_verify_attention
  *   -> (the model's output head) -> splash_choose_targets
  *   -> splash_accept_commit -> splash_token_state_add
  * These are this library's own: the Splash pages describe none of them. All
@@ -437,6 +437,20 @@ int splash_verify_attention_fixed_scratch(const uint16_t* q, int num_q_tokens,
  * SPLASH_DEVICE_BAD_PAGE and maps no slot. *free_count is cut to
  * [0, free_capacity]. num_pages * P must fit 32 bits. Page numbers only: no pool
  * is touched.
+ *
+ * A sequence without slots must not be attended and committed: its block is not
+ * in the cache. splash_build_tables leaves it to the caller to take such
+ * sequences out of block_lens (after a read of device_status).
+ * splash_build_tables_served does it on the device: the same decisions, and
+ *   served_lens [num_seqs] (may be block_lens): T_b of a sequence whose block has
+ *     its pages, 0 of the others. q_offsets is the exclusive prefix of served_lens,
+ *     and positions and slots are packed by it (a sequence without slots has no
+ *     rows).
+ * With served_lens for block_lens in the calls that follow, and tokens packed by
+ * q_offsets, every other sequence is idle in the step: not attended, its context
+ * length and token history as they were, accepted = 0, next_tokens = -1. It may
+ * submit the same block again. (A bad page id is reported and leaves its sequence
+ * served.)
  */
 int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
                         int num_tokens, int page_size, int num_pages, int32_t* page_table,
@@ -445,6 +459,15 @@ int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, 
                         const int32_t* free_count, int32_t* free_count_out, int32_t* q_offsets,
                         int32_t* new_offsets, int32_t* positions, int32_t* slots,
                         int* device_status, struct CUstream_st* stream);
+int splash_build_tables_served(const int32_t* context_lens, const int32_t* block_lens,
+                               int num_seqs, int num_tokens, int page_size, int num_pages,
+                               int32_t* page_table, int max_pages_per_seq,
+                               const int32_t* page_counts, int32_t* page_counts_out,
+                               const int32_t* free_pages, int free_capacity,
+                               const int32_t* free_count, int32_t* free_count_out,
+                               int32_t* q_offsets, int32_t* new_offsets, int32_t* positions,
+                               int32_t* slots, int32_t* served_lens, int* device_status,
+                               struct CUstream_st* stream);
 
 /*
  * splash_release_pages — put the pages past ceil(keep_lens[b] / P) of every

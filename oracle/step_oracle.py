@@ -20,16 +20,18 @@ def pages_of(tokens: int) -> int:
     return -(-tokens // PAGE)
 
 
-def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages):
+def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages, served=None):
     """(table, counts, free_count, q_offsets, new_offsets, positions, slots,
-    set of device codes) after the call; the inputs are not changed."""
+    set of device codes) after the call; the inputs are not changed. With a list
+    `served`, that list gets the served block lengths, and the rows are packed by
+    them."""
     table, counts = np.array(table, np.int64), [int(c) for c in counts]
     B, max_pages = len(ctx), table.shape[1]
     codes = set()
     stack = [int(p) for p in free[:max(0, min(int(free_count), len(free)))]]
     q_off, new_off = [0], [0]
     pos, slots = np.zeros(num_tokens, np.int64), np.full(num_tokens, -1, np.int64)
-    asked = 0                       # pages that this and earlier sequences want
+    asked = asked_rows = 0          # pages and rows that this and earlier sequences want
     had = len(stack)
     for b in range(B):
         c, t, have = int(ctx[b]), int(T[b]), counts[b]
@@ -37,10 +39,10 @@ def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages)
         bad = t < 0 or c < 0 or c + t > max_pages * PAGE or not 0 <= have <= max_pages
         if bad:
             codes.add(BAD_LENGTH)
-        q_off.append(q_off[-1] + rows)
         need = 0 if bad or rows == 0 else max(0, pages_of(c + t) - have)
         asked += need
-        fits = q_off[-1] <= num_tokens
+        asked_rows += rows
+        fits = asked_rows <= num_tokens
         if rows and not fits:
             codes.add(BAD_LENGTH)
         got = 0
@@ -55,7 +57,12 @@ def build_tables(ctx, T, table, counts, free, free_count, num_tokens, num_pages)
             codes.add(OUT_OF_PAGES)
         counts[b] += got
         new_off.append(new_off[-1] + got)
-        if not bad and fits and pages_of(c + t) <= counts[b]:
+        ok = not bad and fits and pages_of(c + t) <= counts[b]
+        if served is not None:
+            served.append(rows if ok else 0)
+            rows = served[-1]
+        q_off.append(q_off[-1] + rows)
+        if ok:
             for i in range(rows):
                 page = int(table[b, (c + i) // PAGE])
                 if not 0 <= page < num_pages:

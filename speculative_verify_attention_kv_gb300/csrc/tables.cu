@@ -8,7 +8,9 @@
 // free_pages[free - 1 - (incl_b - need_b + i)], the top of the stack first. The
 // sequences that get pages are therefore a prefix of those that need some, and
 // every place follows from one prefix sum: no atomics, the same result each
-// time. Release is the same sum over the pages that sequences give back.
+// time. Where the caller takes the served block lengths (T_b, or 0 for a sequence
+// without slots), a second sum over them packs the rows. Release is the same sum
+// over the pages that sequences give back.
 //
 // A first kernel of one CTA does the prefix sums (128 threads for up to 128
 // sequences, 1024 above: fewer warps make its barriers cheaper). The entries
@@ -52,6 +54,7 @@ struct TablesParams {
   int32_t* new_off;            // [B + 1]
   int32_t* positions;
   int32_t* slots;
+  int32_t* served;             // [B], may be T, or nullptr: rows are packed by T
   int vec;                     // positions and slots are 16-byte aligned
   int* status;
 };
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(N) tables_scan_kernel(TablesParams p, int fill
   const int free_now = max(0, min(*p.free_count, p.free_cap));
   const bool in_smem = B <= kSmemSeqs;
   long long rows = 0, needed = 0, taken = 0;     // running sums before this chunk
+  long long packed = 0;                          // rows of the served sequences
   for (int base = 0; base < B; base += N) {
     const int b = base + tid;
     int ctx = 0, T = 0, have = 0;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(N) tables_scan_kernel(TablesParams p, int fill
     }
     const long long want = bad || T == 0 ? 0 : pages_of((long long)ctx + T) - have;
     const long long need = want > 0 ? want : 0;
-    Sums total;
+    Sums total, total_served;
     const Sums incl = block_inclusive<N>(Sums{T, need}, s_sums, &total);
     const long long row1 = rows + incl.a, need1 = needed + incl.b;
     const bool fits = row1 <= p.num_tokens;
@@ -233,8 +237,15 @@ __global__ void __launch_bounds__(N) tables_scan_kernel(TablesParams p, int fill
     if (b < B && fits && !given && need > 0) report(p.status, SPLASH_DEVICE_OUT_OF_PAGES);
     const long long here = block_max<N>(given ? need1 : 0, s_max);
     taken = here > taken ? here : taken;
+    long long row0 = row1 - T;
+    if (p.served) {                              // rows of the others have no place
+      const int T_b = !bad && fits && (given || need == 0) ? T : 0;
+      row0 = packed + block_inclusive<N>(Sums{T_b, 0}, s_sums, &total_served).a - T_b;
+      packed += total_served.a;
+      if (b < B) p.served[b] = T_b;
+    }
     if (b < B) {
-      const long long row0 = row1 - T, need0 = need1 - need;
+      const long long need0 = need1 - need;
       const int off = (int)(row0 < INT_MAX ? row0 : INT_MAX);
       p.q_off[b] = off;
       const int noff = (int)(need0 < taken ? need0 : taken);
@@ -249,7 +260,8 @@ __global__ void __launch_bounds__(N) tables_scan_kernel(TablesParams p, int fill
     needed += total.b;
   }
   if (tid == 0) {
-    const int off = (int)(rows < INT_MAX ? rows : INT_MAX);
+    const long long all = p.served ? packed : rows;
+    const int off = (int)(all < INT_MAX ? all : INT_MAX);
     p.q_off[B] = off;
     p.new_off[B] = (int)taken;
     if (in_smem) {
@@ -369,15 +381,13 @@ bool lengths_args_ok(int num_seqs, int num_pages, int max_pages, int free_cap) {
 
 using namespace splash;
 
-extern "C" {
-
-int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
+static int build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
                         int num_tokens, int page_size, int num_pages, int32_t* page_table,
                         int max_pages_per_seq, const int32_t* page_counts,
                         int32_t* page_counts_out, const int32_t* free_pages, int free_capacity,
                         const int32_t* free_count, int32_t* free_count_out, int32_t* q_offsets,
                         int32_t* new_offsets, int32_t* positions, int32_t* slots,
-                        int* device_status, struct CUstream_st* stream) {
+                        int32_t* served_lens, int* device_status, struct CUstream_st* stream) {
   if (num_tokens < 0 || !lengths_args_ok(num_seqs, num_pages, max_pages_per_seq, free_capacity))
     return SPLASH_ERR_INVALID_ARGUMENT;
   if (page_size != kPageSize) return SPLASH_ERR_UNSUPPORTED;
@@ -388,7 +398,7 @@ int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, 
     return SPLASH_ERR_INVALID_ARGUMENT;
   TablesParams p{context_lens, block_lens, num_seqs, num_tokens, num_pages, page_table,
                  max_pages_per_seq, page_counts, page_counts_out, free_pages, free_capacity,
-                 free_count, free_count_out, q_offsets, new_offsets, positions, slots,
+                 free_count, free_count_out, q_offsets, new_offsets, positions, slots, served_lens,
                  aligned16(positions) && aligned16(slots), device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int fused = num_tokens <= kFusedTokens;
@@ -407,6 +417,37 @@ int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, 
                  cudaSuccess
              ? SPLASH_OK
              : SPLASH_ERR_CUDA;
+}
+
+extern "C" {
+
+int splash_build_tables(const int32_t* context_lens, const int32_t* block_lens, int num_seqs,
+                        int num_tokens, int page_size, int num_pages, int32_t* page_table,
+                        int max_pages_per_seq, const int32_t* page_counts,
+                        int32_t* page_counts_out, const int32_t* free_pages, int free_capacity,
+                        const int32_t* free_count, int32_t* free_count_out, int32_t* q_offsets,
+                        int32_t* new_offsets, int32_t* positions, int32_t* slots,
+                        int* device_status, struct CUstream_st* stream) {
+  return build_tables(context_lens, block_lens, num_seqs, num_tokens, page_size, num_pages,
+                      page_table, max_pages_per_seq, page_counts, page_counts_out, free_pages,
+                      free_capacity, free_count, free_count_out, q_offsets, new_offsets, positions,
+                      slots, nullptr, device_status, stream);
+}
+
+int splash_build_tables_served(const int32_t* context_lens, const int32_t* block_lens,
+                               int num_seqs, int num_tokens, int page_size, int num_pages,
+                               int32_t* page_table, int max_pages_per_seq,
+                               const int32_t* page_counts, int32_t* page_counts_out,
+                               const int32_t* free_pages, int free_capacity,
+                               const int32_t* free_count, int32_t* free_count_out,
+                               int32_t* q_offsets, int32_t* new_offsets, int32_t* positions,
+                               int32_t* slots, int32_t* served_lens, int* device_status,
+                               struct CUstream_st* stream) {
+  if (num_seqs > 0 && !served_lens) return SPLASH_ERR_INVALID_ARGUMENT;
+  return build_tables(context_lens, block_lens, num_seqs, num_tokens, page_size, num_pages,
+                      page_table, max_pages_per_seq, page_counts, page_counts_out, free_pages,
+                      free_capacity, free_count, free_count_out, q_offsets, new_offsets, positions,
+                      slots, served_lens, device_status, stream);
 }
 
 int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* page_table,

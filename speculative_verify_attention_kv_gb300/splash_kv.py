@@ -81,6 +81,8 @@ def _load() -> ctypes.CDLL:
     L = ctypes.c_longlong
     lib.splash_build_tables.restype = I
     lib.splash_build_tables.argtypes = [P, P, I, I, I, I, P, I, P, P, P, I, P, P, P, P, P, P, P, P]
+    lib.splash_build_tables_served.restype = I
+    lib.splash_build_tables_served.argtypes = lib.splash_build_tables.argtypes[:18] + [P, P, P]
     lib.splash_release_pages.restype = I
     lib.splash_release_pages.argtypes = [P, I, P, I, I, P, P, P, I, P, P, P, P, P]
     lib.splash_qkv_append.restype = I
@@ -110,7 +112,7 @@ EXPORTED = ("splash_status_string", "splash_abi_version", "splash_tensor_path_su
             "splash_verify_attention_shared_workspace_size", "splash_verify_attention_shared",
             "splash_verify_attention_shared_profiled",
             "splash_verify_attention_fixed_scratch_bytes", "splash_verify_attention_fixed_scratch",
-            "splash_build_tables", "splash_release_pages", "splash_qkv_append",
+            "splash_build_tables", "splash_build_tables_served", "splash_release_pages", "splash_qkv_append",
             "splash_kv_gather", "splash_token_state_stride", "splash_token_state_add",
             "splash_choose_targets_workspace_size", "splash_choose_targets")
 
@@ -419,11 +421,14 @@ def _pool_on(k_pages, v_pages, dev: int):
 def splash_build_tables(context_lens, block_lens, page_table, page_counts, free_pages, free_count,
                         q_offsets, new_offsets, positions, slots, num_pages: int,
                         page_counts_out=None, free_count_out=None, device_status=None,
-                        stream=None) -> None:
+                        stream=None, served_lens=None) -> None:
     """Pages for the block of every sequence, positions and slots of its tokens.
     ``page_counts`` and ``free_count`` are updated in place unless their
     ``_out`` tensors are given. ``positions`` / ``slots``: int32 [num_tokens],
-    possibly longer than sum(block_lens) (the tail gets slot -1)."""
+    possibly longer than sum(block_lens) (the tail gets slot -1). With
+    ``served_lens`` (int32 [num_seqs], may be ``block_lens``) the block lengths of
+    the sequences that got their pages, 0 of the others, and rows packed by them:
+    what the rest of the step takes in place of ``block_lens``."""
     counts_out = page_counts if page_counts_out is None else page_counts_out
     free_out = free_count if free_count_out is None else free_count_out
     i32 = torch.int32
@@ -432,19 +437,25 @@ def splash_build_tables(context_lens, block_lens, page_table, page_counts, free_
                       (counts_out, "page_counts_out", i32, 1), (free_pages, "free_pages", i32, 1),
                       (free_count, "free_count", i32, 1), (free_out, "free_count_out", i32, 1),
                       (q_offsets, "q_offsets", i32, 1), (new_offsets, "new_offsets", i32, 1),
-                      (positions, "positions", i32, 1), (slots, "slots", i32, 1)), device_status)
+                      (positions, "positions", i32, 1), (slots, "slots", i32, 1),
+                      (served_lens, "served_lens", i32, 1)), device_status)
     B, n = context_lens.shape[0], slots.shape[0]
     if block_lens.shape[0] != B or page_table.shape[0] != B or page_counts.shape[0] != B \
             or counts_out.shape[0] != B or q_offsets.shape[0] != B + 1 \
             or new_offsets.shape[0] != B + 1 or positions.shape[0] != n \
-            or free_count.shape[0] != 1 or free_out.shape[0] != 1:
+            or free_count.shape[0] != 1 or free_out.shape[0] != 1 \
+            or (served_lens is not None and served_lens.shape[0] != B):
         raise ValueError("shape mismatch between the lengths, tables, offsets and slots")
-    st = LIB.splash_build_tables(
+    args = (
         context_lens.data_ptr(), block_lens.data_ptr(), B, n, PAGE_SIZE, int(num_pages),
         page_table.data_ptr(), page_table.shape[1], page_counts.data_ptr(), counts_out.data_ptr(),
         free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), free_out.data_ptr(),
-        q_offsets.data_ptr(), new_offsets.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-        _data(device_status), _raw_stream(stream, dev))
+        q_offsets.data_ptr(), new_offsets.data_ptr(), positions.data_ptr(), slots.data_ptr())
+    end = _data(device_status), _raw_stream(stream, dev)
+    if served_lens is None:
+        st = LIB.splash_build_tables(*args, *end)
+    else:
+        st = LIB.splash_build_tables_served(*args, served_lens.data_ptr(), *end)
     if st != 0:
         raise SplashError(st, "splash_build_tables")
 
