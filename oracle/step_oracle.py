@@ -129,12 +129,15 @@ def norm_rotate(x, weight, eps, inv_freq, axis, positions, interleaved, rope_sca
 
 
 def history(state, tokens, q_offsets, vocab, accepted=None, prompt=False, reset=False):
-    """The int16 token history after a call, as int64."""
+    """The int16 token history after a call, as int64. A sequence whose offsets are
+    not usable has no tokens."""
     state = np.array(state, np.int64)
     if reset:
         state[:] = 0
     for b in range(len(q_offsets) - 1):
         end = q_offsets[b + 1]
+        if not 0 <= q_offsets[b] <= end <= len(tokens):
+            continue
         if accepted is not None:
             end = max(q_offsets[b], min(end, q_offsets[b] + int(accepted[b]) + 1))
         for i in range(q_offsets[b], end):

@@ -721,25 +721,13 @@ __device__ inline int counted_end(const HistoryParams& p, int b, int* lo, bool t
   return end;
 }
 
-// Adds the tokens to the rows in place, one token a thread. Equal tokens of a
-// warp are counted once with their number; the 16-bit counter is moved by a
-// compare-and-swap of its word, because it must stop at 32767. Sums of ones:
-// the order changes nothing.
-__global__ void __launch_bounds__(kThreads) history_add_kernel(HistoryParams p) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  const int lane = threadIdx.x & 31;
-  int b = -1, tok = -1, lo;
-  if (blockIdx.x == 0 && p.status)
-    for (int c = threadIdx.x; c < p.num_seqs; c += kThreads) counted_end(p, c, &lo, true);
-  if (i < p.num_tokens && p.num_seqs > 0 && i >= p.q_off[0] && i < p.q_off[p.num_seqs]) {
-    b = upper_index(p.q_off, p.num_seqs, i);
-    const int end = b < p.num_seqs ? counted_end(p, b, &lo, false) : 0;
-    if (b < p.num_seqs && i >= lo && i < end) tok = p.tokens[i];
-    if (tok < 0 || tok >= p.vocab) tok = -1;
-  }
+// Counts the warp's tokens into row b of each lane (tok < 0: none). Equal tokens are
+// counted once with their number; the 16-bit counter is moved by a compare-and-swap
+// of its word, because it must stop at 32767. Sums of ones: the order changes nothing.
+__device__ inline void count_tokens(const HistoryParams& p, int b, int tok) {
   const unsigned long long at = tok < 0 ? ~0ull : (unsigned long long)b * p.stride + tok;
   const uint32_t same = __match_any_sync(kAll, at);
-  if (tok < 0 || lane != __ffs(same) - 1) return;
+  if (tok < 0 || (int)(threadIdx.x & 31) != __ffs(same) - 1) return;
   // rows are 128 bytes apart at least, and the base is 16-byte aligned
   unsigned int* word = reinterpret_cast<unsigned int*>(p.state) + (at >> 1);
   const int sh = (int)(at & 1) * 16;
@@ -757,6 +745,45 @@ __global__ void __launch_bounds__(kThreads) history_add_kernel(HistoryParams p) 
     const unsigned seen = atomicCAS(word, old, next);
     if (seen == old) return;
     old = seen;
+  }
+}
+
+// Adds the tokens to the rows in place, one token a thread, its sequence found by a
+// search. That takes offsets in order; where some are not (their sequences are not
+// usable, the others are), every sequence is asked whether it has the row.
+constexpr int kSmemOffsets = 2048;
+__global__ void __launch_bounds__(kThreads) history_add_kernel(HistoryParams p) {
+  __shared__ int32_t s_off[kSmemOffsets + 1];
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  const int tok = i < p.num_tokens ? p.tokens[i] : -1;
+  const int B = p.num_seqs;
+  const bool in_smem = B <= kSmemOffsets;
+  int lo, in_order = 1;
+  if (in_smem && threadIdx.x == 0) s_off[0] = p.q_off[0];
+#pragma unroll 4
+  for (int c = threadIdx.x; c < B; c += kThreads) {
+    const int first = p.q_off[c], next = p.q_off[c + 1];
+    in_order &= first <= next;
+    if (in_smem) s_off[c + 1] = next;
+  }
+  if (blockIdx.x == 0 && p.status)
+    for (int c = threadIdx.x; c < B; c += kThreads) counted_end(p, c, &lo, true);
+  in_order = __syncthreads_and(in_order);
+  auto take = [&](int b) {           // b < 0: of no sequence; the whole warp calls it
+    bool in = false;
+    if (b >= 0 && tok >= 0 && tok < p.vocab) {
+      const int end = counted_end(p, b, &lo, false);
+      in = i >= lo && i < end;
+    }
+    count_tokens(p, b, in ? tok : -1);
+  };
+  if (in_order) {
+    const int32_t* off = in_smem ? s_off : p.q_off;
+    const int b = i >= off[0] && i < off[B] ? upper_index(off, B, i) : -1;
+    take(b);
+  } else {
+#pragma unroll 1
+    for (int b = 0; b < B; ++b) take(b);
   }
 }
 
