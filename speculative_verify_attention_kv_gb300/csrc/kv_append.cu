@@ -5,9 +5,9 @@
 // tokens (one token when Hkv >= 8, its warps then loop over the heads). A row
 // of D fp32 values is spread over the 32 lanes (D/32 consecutive values per
 // lane, 16-byte loads), its absmax is a warp max, and each lane writes its D/32
-// codes as one store (splash_quant.cuh).
+// codes as one store. Scale and quotient use correctly rounded fp32 division (no fast-math
+// in this translation unit), rounding is half-to-even (cvt.rni).
 #include "splash_common.cuh"
-#include "splash_quant.cuh"
 
 namespace splash {
 
@@ -57,7 +57,26 @@ __device__ inline void quantise_store(const float (&x)[EPL], int8_t* codes_dst, 
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) a = fmaxf(a, fabsf(x[i]));
-  store_codes<EPL>(x, warp_max(a), codes_dst, scale_dst, lane == 0);
+  a = warp_max(a);
+  const float s = __fdiv_rn(a, 127.0f);
+  uint32_t packed[(EPL + 3) / 4] = {};
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    int c = 0;
+    if (s != 0.f) {
+      c = __float2int_rn(__fdiv_rn(x[i], s));
+      c = max(-127, min(127, c));
+    }
+    packed[i / 4] |= (uint32_t)(c & 0xff) << (8 * (i % 4));
+  }
+  if constexpr (EPL == 2) {
+    *reinterpret_cast<uint16_t*>(codes_dst) = (uint16_t)packed[0];
+  } else if constexpr (EPL == 4) {
+    *reinterpret_cast<uint32_t*>(codes_dst) = packed[0];
+  } else {
+    *reinterpret_cast<uint2*>(codes_dst) = make_uint2(packed[0], packed[1]);
+  }
+  if (lane == 0) *scale_dst = s;
 }
 
 template <int D, typename TIn>
