@@ -25,7 +25,7 @@
 // lane: columns 4l.. and R/2 + 4l.. (interleaved: 8 columns in a row). So the
 // rotation needs no exchange between lanes, a lane has 4 angles for the token,
 // the same for every head, and the cosines, sines, norm weights and frequencies
-// stay in registers: no shared memory, no barrier.
+// stay in registers, without exchange through shared memory.
 //
 // By its bytes it is bound by HBM, but with 8192 values to a 16 KB token the
 // instructions come close, so they are what the layout saves. Products run on
@@ -40,13 +40,16 @@
 // the one worked on. A lane reads only what it copied, so the ring needs no barrier.
 //
 // Measured, 32768 tokens of 24 + 2 x 4 heads of 256, bf16, normed and rotated (973
-// MB): 158 us, 6.2 TB/s, 91% of the measured copy rate. One batch ahead in registers
-// instead of the ring: 174 us (a first version with a lane to 8 columns in a row,
-// shuffled partners and divided codes: 317 us). 2, 4 and 6 stages 173, 160 and 160
-// us; with fp32 inputs 3 stages 228 us, 4 245 us. Batches of 2 rows at 16, 20 or 24
-// warps to an SM: 174, 180, 181 us; 20 warps with batches of 4 spill: 193 us. Heads
-// of 128 98 us and of 64 66 us for the same tokens: there the instructions bound it.
-// 455 tokens: 8.2 us, a chain of loads and angles.
+// MB): 156 us, 6.2 TB/s, 92% of the measured copy rate; fp32 226 us. Heads of 128 98 us
+// and of 64 68 us for the same tokens, 8 + 2 x 1 heads of 128 67 us and of 64 50 us.
+// 455 tokens: 7.4 us, a chain of loads and angles. Lanes without a head on the
+// quantiser's fast path and a division for the values next to a border alone: with
+// all 8 values of such a lane divided 158, 226, 102, 70, 81, 64 and 8.2 us.
+// Earlier, at 158 us: one batch ahead in registers instead of the ring 174 us (a first
+// version with a lane to 8 columns in a row, shuffled partners and divided codes: 317
+// us). 2, 4 and 6 stages 173, 160 and 160 us; with fp32 inputs 3 stages 228 us, 4 245
+// us. Batches of 2 rows at 16, 20 or 24 warps to an SM: 174, 180, 181 us; 20 warps with
+// batches of 4 spill: 193 us.
 #include <cmath>
 #include <type_traits>
 

@@ -1,8 +1,8 @@
 // The cache's row quantiser as splash_qkv_append uses it. splash_kv_append divides
-// every value: it has fewer instructions around it, and with the quotients below one
-// value next to a border in a warp's row costs more than the divisions that the
-// others save (256 tokens of 4 heads of 256: 4.7 us instead of 4.1, 32768 bf16 tokens
-// 93 instead of 82, rows of zeros 100 instead of 67; fp32 random rows 71 instead of 82).
+// every value: with fewer instructions around it, the quotients below gain little
+// and lose where values are next to a border (32768 tokens of 4 heads of 256: fp32
+// 70 us instead of 82, bf16 82 either way, rows of zeros 73 instead of 67, of zeros and
+// NaN 88 instead of 67; 256 bf16 tokens 5.0 instead of 4.1).
 //
 // A row of D values is spread over LPR lanes of a warp (EPL = D / LPR
 // consecutive values a lane): a = max |x| over the row's lanes, s = fl32(a/127),
@@ -51,12 +51,14 @@ static __device__ __noinline__ uint32_t code_exact(float x, float s) {
 // x * fl(1/s), off by at most 127 * 2^-23 from x / s, and rounded by adding 1.5 *
 // 2^23; fl32(x / s) itself is off by at most 127 * 2^-24. Together that is below
 // 2.4e-5, so a value whose fraction is further than 4e-5 from a half has the
-// same code either way. The others (one head row in 50), and zero, infinite or
-// NaN rows, whose product is not finite, are divided.
+// same code either way. The others (of random fp32 values one in 12500) are divided,
+// and so are products that are not finite (infinite and NaN values). Where s = 0, the
+// reciprocal is taken as 0, and so are the codes: a row of zeros, or a lane that has
+// no head.
 template <int EPL>
 __device__ inline void quantise(const float (&x)[EPL], float s, uint32_t (&packed)[(EPL + 3) / 4]) {
   constexpr float kRound = 12582912.f;
-  const float inv = __frcp_rn(s);
+  const float inv = s != 0.f ? __frcp_rn(s) : 0.f;
   uint32_t c[EPL];
   bool sure = true;
 #pragma unroll
@@ -73,7 +75,10 @@ __device__ inline void quantise(const float (&x)[EPL], float s, uint32_t (&packe
   }
   if (!sure) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = code_exact(x[i], s);
+    for (int i = 0; i < EPL; ++i) {
+      const float q = __fmul_rn(x[i], inv), n = __fsub_rn(__fadd_rn(q, kRound), kRound);
+      if (!(fabsf(__fsub_rn(q, n)) <= 0.49996f)) c[i] = code_exact(x[i], s);
+    }
   }
 #pragma unroll
   for (int i = 0; i < EPL; i += 4) {
