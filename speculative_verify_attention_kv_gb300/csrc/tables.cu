@@ -13,10 +13,10 @@
 // over the pages that sequences give back.
 //
 // A first kernel of one CTA does the prefix sums (128 threads for up to 128
-// sequences, 1024 above: fewer warps make its barriers cheaper). The entries
-// and the slot map are then one independent write each. Small calls write them
-// in the same CTA; larger ones in a second kernel over the whole GPU, which
-// starts under the first (programmatic dependent launch). What bounds both is
+// sequences, 1024 above: fewer warps make its barriers cheaper, 128 sequences of 8
+// rows 4.7 us, 129 of one row 9.7). The entries and the slot map are then one
+// independent write each. Small calls write them in the same CTA; larger ones in a
+// second kernel over the whole GPU, which starts under the first (programmatic dependent launch). What bounds both is
 // latency, a chain of five or six dependent loads: a step of 64 sequences (449
 // slots) takes 5.4 us in one CTA; the admission of 1.96 million tokens (17 MB, 2.5
 // us at the measured copy rate) 2.0 us for the sums and 7 us for the fill; the
@@ -366,9 +366,19 @@ __global__ void __launch_bounds__(kFillThreads) release_fill_kernel(ReleaseParam
                 (long long)gridDim.x * kFillThreads);
 }
 
-// Up to this many slots (build) or table entries (release) one CTA writes them
-// itself.
-constexpr long long kFusedTokens = 4096, kFusedEntries = 16384;
+// Up to this many slots (build) or table entries (release) the scan's CTA writes them
+// itself, more are a second kernel's. us, one CTA / two kernels:
+//   128 threads  build 448 rows 4.7 / 5.8, 1024 rows 4.3 to 5.4 / 4.7 to 5.1, 1536 rows 6.6 to
+//                7.0 / 4.9 to 5.4, 4096 rows 8.4 to 9.0 / 4.9 to 5.2; release of a quarter of 1024
+//                entries 2.8 to 3.3 / 3.6 to 3.8, of 4096 5.5 / 3.7, of 16384 7.5 / 3.9
+//   1024 threads build 512 rows 10.3 / 11.6, 2048 rows 8.3 to 9.6 / 9.3 to 10.8, 4096 rows 9.0 to
+//                9.7 / 9.6 to 10.1, 8192 rows 11.2 / 9.8; release of a quarter of 4096 entries
+//                5.8 / 6.9, of 16384 8.0 to 8.7 / 6.5 to 7.2
+constexpr long long kFusedSmall = 1024, kFusedLarge = 4096;
+
+bool one_cta(int num_seqs, long long items) {
+  return items <= (num_seqs <= kScanSmall ? kFusedSmall : kFusedLarge);
+}
 
 bool lengths_args_ok(int num_seqs, int num_pages, int max_pages, int free_cap) {
   // a slot is page * 16 + offset in 32 bits; table places times 16 too
@@ -401,8 +411,8 @@ static int build_tables(const int32_t* context_lens, const int32_t* block_lens, 
                  free_count, free_count_out, q_offsets, new_offsets, positions, slots, served_lens,
                  aligned16(positions) && aligned16(slots), device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int fused = num_tokens <= kFusedTokens;
-  if (num_seqs <= kScanSmall && (!fused || num_tokens <= 4 * kScanSmall * kTokensPerThread))
+  const int fused = one_cta(num_seqs, num_tokens);
+  if (num_seqs <= kScanSmall)
     tables_scan_kernel<kScanSmall><<<1, kScanSmall, 0, s>>>(p, fused);
   else
     tables_scan_kernel<kScanLarge><<<1, kScanLarge, 0, s>>>(p, fused);
@@ -467,8 +477,8 @@ int splash_release_pages(const int32_t* keep_lens, int num_seqs, const int32_t* 
                   released_offsets, device_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long most = (long long)num_seqs * max_pages_per_seq;
-  const int fused = most <= kFusedEntries;
-  if (num_seqs <= kScanSmall && (!fused || most <= 8 * kScanSmall))
+  const int fused = one_cta(num_seqs, most);
+  if (num_seqs <= kScanSmall)
     release_scan_kernel<kScanSmall><<<1, kScanSmall, 0, s>>>(p, fused);
   else
     release_scan_kernel<kScanLarge><<<1, kScanLarge, 0, s>>>(p, fused);
