@@ -6,8 +6,9 @@
 // or 4 fp32), so that the writes, two thirds of the bytes or more, are full
 // sectors in order. What hides the latency is residency: every thread of the GPU
 // with kUnroll pieces of K and V in flight. 131072 rows of 4 heads of 256, bf16
-// (810 MB): 2 pieces and 8 CTAs to an SM 130 us, 92% of the measured copy rate;
-// 4 pieces at the 4 CTAs that their registers leave 145 us, 8 pieces 212 us.
+// (810 MB): 2 pieces and 8 CTAs to an SM 130 us, 92% of the measured copy rate (32
+// registers a thread, of which the bf16 forms spill 36 bytes); 4 pieces at the 4 CTAs
+// that their registers leave 145 us, 8 pieces 212 us.
 #include "splash_common.cuh"
 #include "splash_host.cuh"
 

@@ -15,9 +15,10 @@
 // each step rounded to fp32. The choice is the lowest index of the largest z5
 // above -inf (NaN is never chosen), -1 where there is none.
 //
-// By its bytes the logits, read once, bound it. In fact it is bound by
-// instructions and latency: a step's rows are few, and everything before the
-// logits (offsets, state, biases, masks) is a chain of loads. So a warp works for
+// By its bytes the logits, read once, bound it. In fact neither memory nor the issue
+// slots are full (2 of 4 instructions a clock): a step's rows are few, everything before
+// the logits (offsets, state, biases, masks) is a chain of loads, and the largest
+// stall after that is the wait for the instruction before. So a warp works for
 // itself, without block barriers: it takes a run of segments of the vocabulary
 // (1024 tokens) for up to 8 rows of a sequence. Of a segment only few tokens
 // are touched by a penalty or a bias ("special"). It marks them in a bitmap, lists
@@ -791,8 +792,8 @@ __global__ void __launch_bounds__(kThreads) history_add_kernel(HistoryParams p) 
 // the sequence's tokens in it in shared memory and writes the window whole, 16
 // bytes at a time. Bound by the latency of one CTA's few steps: 16 sequences of 512
 // to 32768 tokens, 131072 entries (5 MB) 5.2 us; with 160 windows instead of 144, so
-// that 8 SMs take two in turn, 7.7 us. 32 registers let two CTAs share an SM: 256
-// sequences 32 us instead of 45.
+// that 8 SMs take two in turn, 7.7 us. 32 registers (4 bytes spilled) let two CTAs share
+// an SM: 256 sequences 32 us instead of 45.
 __global__ void __launch_bounds__(1024, 2) history_reset_kernel(HistoryParams p, int span, int windows) {
   extern __shared__ __align__(16) int s_n[];
   const int b = blockIdx.x / windows, lo_v = blockIdx.x % windows * span;
