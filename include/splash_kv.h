@@ -554,7 +554,8 @@ int splash_kv_gather(const int8_t* k_pages, const int8_t* v_pages, const float* 
  * called before or after it). prompt != 0 sets bit 15 instead of counting.
  * reset != 0 clears every sequence's row first, whole (a call over the rows of
  * newly admitted sequences). Tokens outside [0, vocab) are passed over. A
- * sequence with unusable offsets reports SPLASH_DEVICE_BAD_LENGTH.
+ * sequence with unusable offsets reports SPLASH_DEVICE_BAD_LENGTH and has no
+ * tokens; the others are counted.
  * `state` is 16-byte aligned, state_stride a multiple of 64.
  */
 int splash_token_state_stride(int vocab);
@@ -588,11 +589,13 @@ int splash_token_state_add(const int32_t* tokens, int num_tokens, const int32_t*
  * repetition values must be > 0 and finite (others count as 1), frequency and
  * presence finite.
  * target_tokens[i]: the lowest v with the largest z5 above -inf; -1 where there
- * is none. NaN is never chosen.
+ * is none (splash_accept_commit then hands it on as next token). NaN is never
+ * chosen.
  * out (NULL: not written): fp32 z5 [num_rows, vocab], row stride out_stride; may
  * be the logits themselves (F32, same stride).
  * Rows of no sequence, and of sequences with unusable offsets
- * (SPLASH_DEVICE_BAD_LENGTH), are left as they were. The workspace (256-byte
+ * (SPLASH_DEVICE_BAD_LENGTH), are left as they were. A row that two sequences
+ * claim (offsets out of order) gets unspecified results. The workspace (256-byte
  * aligned) is scratch for the duration of the call.
  */
 size_t splash_choose_targets_workspace_size(int num_rows, int vocab);
