@@ -88,8 +88,10 @@ enum {
                                          call undefined */
   SPLASH_DEVICE_INTERNAL = 4,         /* the tensor-core kernel found its shared memory
                                          misaligned and did nothing */
-  SPLASH_DEVICE_OUT_OF_PAGES = 5      /* the free list cannot serve every sequence
+  SPLASH_DEVICE_OUT_OF_PAGES = 5,     /* the free list cannot serve every sequence
                                          (splash_build_tables) */
+  SPLASH_DEVICE_BAD_TREE = 6          /* a parent that does not come before its node,
+                                         or a path that does not go up in rows */
 };
 
 /* Element types of the entry points that take a dtype argument. */
@@ -608,6 +610,145 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
                           const int32_t* mask, long long mask_stride, int num_masks,
                           const int32_t* mask_rows, float* out, long long out_stride,
                           int32_t* target_tokens, void* workspace, size_t workspace_bytes,
+                          int* device_status, struct CUstream_st* stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of a tree of drafts. Where the draft proposes several
+ * continuations, a sequence's block is a tree of T_b nodes instead of a chain:
+ *   splash_build_tables_served -> splash_tree_masks -> splash_qkv_append (with
+ *   the tree's positions) -> splash_verify_attention_tree -> (the model's output
+ *   head) -> splash_choose_targets -> splash_accept_tree -> splash_kv_compact
+ *   -> splash_token_state_add (path_tokens, accepted) -> splash_release_pages
+ * and splash_token_logprobs (rows = path_rows) for what the step emitted. These
+ * are this library's own: the Splash pages describe none of them. All are
+ * enqueued on `stream`, allocate nothing and can be captured in a graph.
+ *
+ * A tree is `parents`: int32 [num_tokens], rows q_offsets[b] ..
+ * q_offsets[b+1] - 1 those of sequence b (q_offsets as splash_build_tables
+ * writes them). Node 0 is the root: the token that the target produced at the
+ * step before. parents[row] is the place, within its tree, of the node that this
+ * one continues: less than the node's own place, -1 for a node that continues
+ * the context itself (the root; further such nodes are trees of their own beside
+ * it, which are attended but never accepted). At most max_block_len <= 256 nodes.
+ * A parent out of range reports SPLASH_DEVICE_BAD_TREE and counts as -1. A
+ * sequence with unusable offsets reports SPLASH_DEVICE_BAD_LENGTH; its rows, and
+ * rows of no sequence, are left as they were. A chain is parents[t] = t - 1.
+ *
+ * splash_choose_targets counts a block's own tokens x_0 .. x_t for row t, which is
+ * a chain's history: for a tree leave its penalties out, or keep them to committed
+ * tokens by passing block_tokens of -1.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * splash_tree_masks — what every node sees of its tree, and where it stands.
+ *   masks [num_tokens, mask_stride]: bit j % 32 of word j / 32 of row t is set
+ *     where node j is t itself or one of its ancestors. The first
+ *     ceil(max_block_len / 32) words of a row are written.
+ *   depths [num_tokens] (may be NULL): ancestors of the node.
+ *   positions [num_tokens] (may be NULL; needs context_lens): context_lens[b] +
+ *     depth, the position for the rotation. The slot stays the row's own.
+ */
+int splash_tree_masks(const int32_t* parents, int num_tokens, const int32_t* q_offsets,
+                      const int32_t* context_lens, int num_seqs, int max_block_len,
+                      int32_t* masks, int mask_stride, int32_t* depths, int32_t* positions,
+                      int* device_status, struct CUstream_st* stream);
+
+/*
+ * splash_verify_attention_tree — splash_verify_attention under a mask of the block:
+ * node t of sequence b attends to the logical keys j < context_lens[b] and to
+ * those keys context_lens[b] + i, i < T_b, whose bit i is set in its row of
+ * tree_masks [num_q_tokens, mask_stride words]. Any mask will do (bits past T_b
+ * are ignored); splash_tree_masks writes a tree's. A row that sees no key at all
+ * has out = 0 and lse = -inf.
+ *   head_dim 64, 128 or 256, max_block_len <= 256, any G (T_b * G may exceed 128:
+ *   such a sequence takes several row blocks of up to 128 rows, each of which
+ *   reads the keys).
+ *   ctas: 0 automatic, else that many persistent CTAs (at most 1023).
+ * The workspace holds splash_verify_attention_tree_workspace_size bytes (for the
+ * same ctas), 256-byte aligned. Output, determinism and error contract as
+ * splash_verify_attention; q, out and the scales 16-byte aligned. Block lengths
+ * that sum past num_q_tokens report SPLASH_DEVICE_BAD_LENGTH and nothing is
+ * written. Rows of a sequence whose lengths are out of range are left as they were.
+ */
+size_t splash_verify_attention_tree_workspace_size(int num_seqs, int num_q_tokens,
+                                                   int num_q_heads, int num_kv_heads,
+                                                   int head_dim, int max_block_len, int ctas);
+int splash_verify_attention_tree(
+    const uint16_t* q, int num_q_tokens, const int8_t* k_pages, const int8_t* v_pages,
+    const float* k_scales, const float* v_scales, const int32_t* page_table,
+    int max_pages_per_seq, const int32_t* context_lens, const int32_t* block_lens,
+    const int32_t* tree_masks, int mask_stride, int num_seqs, int num_q_heads, int num_kv_heads,
+    int head_dim, int page_size, int num_pages, int max_block_len, float sm_scale, uint16_t* out,
+    float* lse, void* workspace, size_t workspace_bytes, int* device_status,
+    struct CUstream_st* stream, int ctas);
+
+/*
+ * splash_accept_tree — splash_accept_commit for trees: from the root on, the
+ * lowest node that continues the current one and holds the target's choice after
+ * it, block_tokens[j] == target_tokens[current], is accepted and becomes the
+ * current one, until there is none. Nodes with a negative token are never accepted.
+ * With a nodes accepted after the root:
+ *   accepted[b] = a;  next_tokens[b] = target_tokens[current];
+ *   context_lens_out[b] = context_lens[b] + a + 1 (may be context_lens itself);
+ *   path_rows [num_tokens]: for i <= a, row q_offsets[b] + i holds the row of the
+ *     path's i-th node (the root first), the sequence's other rows -1;
+ *   path_tokens [num_tokens] (may be NULL): those nodes' tokens, -1 elsewhere.
+ * A sequence without nodes, or with unusable offsets, gets accepted = 0,
+ * next_tokens = -1 and keeps its length. No output may be one of the other inputs.
+ */
+int splash_accept_tree(const int32_t* block_tokens, const int32_t* parents,
+                       const int32_t* target_tokens, int num_tokens, const int32_t* q_offsets,
+                       const int32_t* context_lens, int32_t* context_lens_out, int32_t* accepted,
+                       int32_t* next_tokens, int32_t* path_rows, int32_t* path_tokens,
+                       int num_seqs, int max_block_len, int* device_status,
+                       struct CUstream_st* stream);
+
+/*
+ * splash_kv_compact — the accepted nodes' cache rows moved together, so that the
+ * committed tokens lie at consecutive positions: for 1 <= i <= accepted[b], with
+ * o = q_offsets[b], slot slots[o + i] receives the K and V codes and scales, bit for
+ * bit, that slot slots[path_rows[o + i]] held before the call, for every KV head and
+ * layer. (slots as splash_build_tables writes them, path_rows and accepted as
+ * splash_accept_tree does. Row o + 0 stays.) Other slots are left as they were.
+ *   num_layers pools of the same shape, code_layer_stride bytes and
+ *   scale_layer_stride floats apart (ignored for one layer); layers share the page
+ *   numbers. code_layer_stride is a multiple of 16, both at least a pool's size.
+ * A path row before o + i or outside the sequence reports SPLASH_DEVICE_BAD_TREE, a
+ * slot past the pool SPLASH_DEVICE_BAD_PAGE; that row is not moved, nor one with a
+ * negative slot. An accepted count past the sequence's rows reports
+ * SPLASH_DEVICE_BAD_LENGTH and moves nothing of it. The slots of a call differ.
+ */
+int splash_kv_compact(int8_t* k_pages, int8_t* v_pages, float* k_scales, float* v_scales,
+                      long long code_layer_stride, long long scale_layer_stride, int num_layers,
+                      const int32_t* slots, const int32_t* path_rows, int num_tokens,
+                      const int32_t* q_offsets, const int32_t* accepted, int num_seqs,
+                      int num_kv_heads, int head_dim, int page_size, int num_pages,
+                      int* device_status, struct CUstream_st* stream);
+
+/*
+ * splash_token_logprobs — log probabilities of given tokens, entropy and the
+ * likeliest tokens of rows of logits.
+ *
+ * logits: `dtype` (F32, BF16 or F16) [num_rows, >= vocab], row stride logits_stride
+ * elements, any alignment. Output i belongs to row r = rows[i] (int32 [num_out]), or
+ * row i when rows is NULL; r < 0: output i is left as it was; r >= num_rows: also,
+ * and SPLASH_DEVICE_BAD_LENGTH. NaN counts as -inf and infinity as the largest
+ * finite fp32. With p = softmax of the row, in fp32:
+ *   logprobs[i] = ln p(tokens[r])  (tokens int32 [num_rows]: by row of the logits,
+ *     as splash_choose_targets writes them; -inf for a token outside the vocabulary;
+ *     tokens and logprobs both NULL: left out)
+ *   entropy[i] = -sum_v p(v) ln p(v)  (NULL: left out)
+ *   top_ids, top_logprobs [num_out, top], top <= 32: the tokens of the largest
+ *     logits and their ln p, the largest first, the lowest index first among equal
+ *     ones; -1 and -inf where fewer tokens are above -inf.
+ * A row with nothing above -inf has log probabilities of -inf and entropy 0.
+ * The workspace (16-byte aligned) is scratch for the duration of the call.
+ */
+size_t splash_token_logprobs_workspace_size(int num_out, int vocab);
+int splash_token_logprobs(const void* logits, int dtype, long long logits_stride, int num_rows,
+                          int vocab, const int32_t* rows, int num_out, const int32_t* tokens,
+                          float* logprobs, float* entropy, int top, int32_t* top_ids,
+                          float* top_logprobs, void* workspace, size_t workspace_bytes,
                           int* device_status, struct CUstream_st* stream);
 
 #ifdef __cplusplus

@@ -83,6 +83,8 @@ cudaError_t counted(cudaError_t e) {
   return e;
 }
 
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+
 }  // namespace splash
 
 using namespace splash;

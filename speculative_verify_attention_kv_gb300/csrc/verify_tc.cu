@@ -54,9 +54,15 @@
 // or one sequence's rows against its keys after the prefix. The item table
 // gives each segment its page-table row, first query token, row offset and
 // key range; the pipeline above is the same.
+// For a tree of drafts (kTree) a unit is (sequence, KV head, row block): trees
+// with more than 128 rows take several. Its rows see the sequence's context and,
+// in the last tiles, the nodes whose bits their masks have: a thread takes the 16
+// bits of its keys from the mask words, once per row and tile, and nothing else
+// of the softmax differs. Only the tiles that hold nodes (5 at most) pay for it.
 #include <type_traits>
 
 #include "splash_groups.cuh"
+#include "splash_tree.cuh"
 #include "tcgen05_ptx.cuh"
 
 namespace splash {
@@ -112,8 +118,9 @@ struct Cfg {
 struct Seg {
   int b, h, i0, i1, T, ctx, Lk, R, u;
   int klo;                        // first key any row of the unit sees
-  int qbase, r0;                  // items only: row r is query token qbase + (r0 + r) / G,
-                                  // head h * G + (r0 + r) % G
+  int qbase, r0;                  // items and trees only: row r is query token
+                                  // qbase + (r0 + r) / G, head h * G + (r0 + r) % G
+  bool whole;                     // trees only: the segment is the whole unit
 };
 
 // The CTA's tiles [t, t_end) of the stream of all units, one segment (a run
@@ -177,22 +184,58 @@ struct ItemSegIter {
   }
 };
 
+// The same over sequences whose rows are cut into row blocks: units are
+// (sequence, KV head, row block), the blocks of a head next to each other.
+struct TreeSegIter {
+  const int* stp;
+  const int* seq_T;
+  const int* seq_ctx;
+  const int* q_off;
+  int B, G, Hkv;
+  int t, t_end;
+  __device__ bool next(Seg& s) {
+    if (t >= t_end) return false;
+    s.b = upper_index(stp, B - 1, t);
+    s.T = seq_T[s.b];
+    s.ctx = seq_ctx[s.b];
+    s.qbase = q_off[s.b];
+    s.Lk = s.ctx + s.T;
+    s.klo = 0;
+    const RowBlocks rb = row_blocks(s.T, G);
+    const int tiles = (s.Lk + kTileKeys - 1) / kTileKeys;
+    const int local = t - stp[s.b];
+    const int unit = local / tiles;
+    s.h = unit / rb.count;
+    s.r0 = (unit - s.h * rb.count) * rb.rows;
+    s.R = min(rb.rows, s.T * G - s.r0);
+    s.i0 = local - unit * tiles;
+    s.i1 = min(tiles, s.i0 + (t_end - t));
+    s.whole = s.i0 == 0 && s.i1 == tiles;
+    s.u = 0;
+    t += s.i1 - s.i0;
+    return true;
+  }
+};
+
 // The plan's workspace layout: the plain one, or the one of a plan with
-// prefix groups (the same names for the regions the kernel reads).
-template <bool kItems>
-__device__ __forceinline__ typename std::conditional<kItems, GroupLayout, WorkspaceLayout>::type
-layout_for(int B, int Hkv, int D, long long rows_bound) {
-  if constexpr (kItems)
+// prefix groups or of trees (the same names for the regions the kernel reads).
+template <bool kItems, bool kTree>
+__device__ __forceinline__ auto layout_for(int B, int Hkv, int D, long long rows_bound) {
+  if constexpr (kTree)
+    return make_tree_layout(B, D, rows_bound);
+  else if constexpr (kItems)
     return make_group_layout(B, Hkv, D, rows_bound);
   else
     return make_layout(B, Hkv, D, rows_bound);
 }
 
-template <bool kItems>
-__device__ __forceinline__ typename std::conditional<kItems, ItemSegIter, SegIter>::type
-make_iter(const int* stp, const int* seq_T, const int* seq_ctx, const ItemDesc* items, int B,
-          int G, int Hkv, int window, int t, int t_end) {
-  if constexpr (kItems)
+template <bool kItems, bool kTree>
+__device__ __forceinline__ auto make_iter(const int* stp, const int* seq_T, const int* seq_ctx,
+                                          const int* q_off, const ItemDesc* items, int B, int G,
+                                          int Hkv, int window, int t, int t_end) {
+  if constexpr (kTree)
+    return TreeSegIter{stp, seq_T, seq_ctx, q_off, B, G, Hkv, t, t_end};
+  else if constexpr (kItems)
     return ItemSegIter{stp, items, max_items(B), G, Hkv, t, t_end};
   else
     return SegIter{stp, seq_T, seq_ctx, B, G, Hkv, window, t, t_end};
@@ -336,7 +379,8 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
   static_assert(kChunks % 4 == 0 && kTileKeys % kKeysPerPass == 0, "converter units");
   const int w = lt >> 5, l = lt & 31, qtr = l >> 3, rsel = (l >> 2) & 1, j = l & 3;
   const int pair = qtr / kQuartersPerPair, qq = qtr % kQuartersPerPair;
-  const int c16 = 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
+  // (a row of 64 codes is 4 chunks: a quarter warp takes both rows whole)
+  const int c16 = D == 64 ? j : 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
   const int key_in_pass = w * (32 * 16 / D) + 2 * pair + rsel;
   uint4 wv[kPer];
 #pragma unroll
@@ -363,10 +407,12 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
 // ------------------------------------------------------------------- kernel
 // kSwa: sliding-window instantiation (window read from the parameters); the
 // plain one compiles the window bounds out. kItems: the plan holds prefix
-// groups, and the kernel walks its item table (never with a window).
-template <int D, bool kSwa, bool kItems>
-__global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
-  static_assert(!(kSwa && kItems), "prefix groups are planned without a window");
+// groups, and the kernel walks its item table (never with a window). kTree: row
+// blocks under tree masks.
+template <int D, bool kSwa, bool kItems, bool kTree>
+__global__ void __launch_bounds__(kThreads, 1)
+verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::type p) {
+  static_assert(kSwa + kItems + kTree <= 1, "prefix groups and trees are planned without a window");
   using C = Cfg<D>;
   static_assert(sizeof(Smem) <= C::kBarBytes, "barrier area");
   extern __shared__ uint8_t smem_raw[];
@@ -433,24 +479,26 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
     return;
   }
   const int B = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
-  const auto L = layout_for<kItems>(B, Hkv, D, hd->rows_bound);
+  const auto L = layout_for<kItems, kTree>(B, Hkv, D, hd->rows_bound);
   const int* q_off = reinterpret_cast<const int*>(p.ws + L.q_off);
   const int* seq_T = reinterpret_cast<const int*>(p.ws + L.seq_T);
   const int* seq_ctx = reinterpret_cast<const int*>(p.ws + L.seq_ctx);
   const ItemDesc* items = static_cast<const ItemDesc*>(nullptr);
   if constexpr (kItems) items = reinterpret_cast<const ItemDesc*>(p.ws + L.items);
   const int* stp = reinterpret_cast<const int*>(p.ws + L.stp) + kClassTensor * (B + 1);
-  const int* nseg = reinterpret_cast<const int*>(p.ws + L.nseg);
-  const int* cfirst = reinterpret_cast<const int*>(p.ws + L.cfirst);
-  const int* part_base = reinterpret_cast<const int*>(p.ws + L.part_base);
+  const int *nseg = nullptr, *cfirst = nullptr, *part_base = nullptr;
+  if constexpr (!kTree) {
+    nseg = reinterpret_cast<const int*>(p.ws + L.nseg);
+    cfirst = reinterpret_cast<const int*>(p.ws + L.cfirst);
+    part_base = reinterpret_cast<const int*>(p.ws + L.part_base);
+  }
   float* o_part = reinterpret_cast<float*>(p.ws + L.o_part);
   float* lse_part = reinterpret_cast<float*>(p.ws + L.lse_part);
 
   const int window = kSwa ? p.window : 0;
   const int* cst = reinterpret_cast<const int*>(p.ws + L.cta_start) + kClassTensor * (kMaxCtas + 1);
-  typename std::conditional<kItems, ItemSegIter, SegIter>::type iter =
-      make_iter<kItems>(stp, seq_T, seq_ctx, items, B, G, Hkv, window, cst[blockIdx.x],
-                        cst[blockIdx.x + 1]);
+  auto iter = make_iter<kItems, kTree>(stp, seq_T, seq_ctx, q_off, items, B, G, Hkv, window,
+                                       cst[blockIdx.x], cst[blockIdx.x + 1]);
 
   if (warp < kSoftmaxWarps) {
     // ===================================================== softmax + epilogue
@@ -484,10 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
         const int i = ln[k] & 31, r = (ln[k] >> 5) * rpq + i;
         live[k] = i < rpq && r < s.R;
         rr[k] = live[k] ? r : -1;
-        if constexpr (kItems) {
+        if constexpr (kItems || kTree) {
           const int j = s.r0 + (live[k] ? r : 0);
           const int tt = j / G, gg = j - tt * G;
-          lim[k] = s.ctx + tt;                            // last visible key of the row
+          // last visible key of the row (of a tree: the row of its mask)
+          lim[k] = kTree ? s.qbase + tt : s.ctx + tt;
           lo[k] = 0;
           qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + gg;
         } else {
@@ -532,9 +581,22 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
           up[k] = __uint_as_float((uint32_t)(e + 127) << 23);
           rowfac[k] = p.sm_scale_log2 / up[k];
         }
-        static_assert((D / 2) % 64 == 0, "Q' stores of 64 packed columns");
+        static_assert(D == 64 || (D / 2) % 64 == 0, "Q' stores of 64 packed columns, or 32");
+        if constexpr (D == 64) {
+          uint32_t v[16];
 #pragma unroll
-        for (int c0 = 0; c0 < D / 2; c0 += 64) {          // 64 packed columns per store
+          for (int i = 0; i < 8; ++i)                     // packed column 4i + quad
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 f =
+                  __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[k][i]));
+              __half2 hv = __floats2half2_rn(f.x * up[k], f.y * up[k]);
+              v[2 * i + k] = *reinterpret_cast<uint32_t*>(&hv);
+            }
+          tmem_st16x128_x8(tmem + lane_base + C::kQCol, v);
+        }
+#pragma unroll
+        for (int c0 = 0; D > 64 && c0 < D / 2; c0 += 64) {   // 64 packed columns per store
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -594,12 +656,23 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
           }
           // tile keys jj with nlo <= jj < nvis are visible to the row
           int nvis[2] = {kTileKeys, kTileKeys}, nlo[2] = {-1, -1};
+          uint32_t vm[2] = {0xffffu, 0xffffu};          // trees: which of this thread's keys
           bool full = true;
           // a tile below the block's keys (and, with a window, above every
           // row's lower bound) is visible to every row: no per-row bounds
           const bool tile_inside = k0 + kTileKeys <= s.ctx &&
                                    (!kSwa || s.ctx + s.T - window <= k0);
-          if (!tile_inside) {
+          if constexpr (kTree) {
+            if (!tile_inside) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (live[k])
+                  vm[k] = tree_bits16(p.tree_masks + (size_t)lim[k] * p.mask_stride,
+                                      k0 + 16 * quad - s.ctx, s.T);
+                full = full && vm[k] == 0xffffu;
+              }
+            }
+          } else if (!tile_inside) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               nvis[k] = live[k] ? min(kTileKeys, lim[k] - k0 + 1) : 0;
@@ -615,8 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int j = 16 * quad + 2 * i;
-                if (j >= nvis[k] || j < nlo[k]) x[k][i].x = -INFINITY;
-                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) x[k][i].y = -INFINITY;
+                if (kTree ? !(vm[k] >> (2 * i) & 1) : (j >= nvis[k] || j < nlo[k]))
+                  x[k][i].x = -INFINITY;
+                if (kTree ? !(vm[k] >> (2 * i + 1) & 1) : (j + 1 >= nvis[k] || j + 1 < nlo[k]))
+                  x[k][i].y = -INFINITY;
               }
           }
           float base[2] = {0.f, 0.f};
@@ -670,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
               float2 vq = vs2[i];
               if (!full) {      // scales of masked keys are not trusted
                 const int j = 16 * quad + 2 * i;
-                if (j >= nvis[k] || j < nlo[k]) vq.x = 0.f;
-                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) vq.y = 0.f;
+                if (kTree ? !(vm[k] >> (2 * i) & 1) : (j >= nvis[k] || j < nlo[k])) vq.x = 0.f;
+                if (kTree ? !(vm[k] >> (2 * i + 1) & 1) : (j + 1 >= nvis[k] || j + 1 < nlo[k]))
+                  vq.y = 0.f;
               }
               const float2 e0 = __ffma2_rn(x[k][i], rf2, nb2);
               const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
@@ -725,7 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
       if (warp_live) {
         // rows go to the output when one CTA covers the unit (and, with
         // prefix groups, the unit is in none: part_base < 0 says both)
-        const int ns = kItems ? (part_base[s.u] < 0 ? 1 : 2) : nseg[s.u];
+        int ns;
+        if constexpr (kTree) ns = s.whole ? 1 : 2;
+        else ns = kItems ? (part_base[s.u] < 0 ? 1 : 2) : nseg[s.u];
         float inv[2];
         long long prow[2];
 #pragma unroll
@@ -735,7 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_tc_kernel(AttnParams p) {
           lt += __shfl_xor_sync(0xffffffffu, lt, 2);
           l[k] = lt;
           inv[k] = lt > 0.f ? 1.f / lt : 0.f;
-          prow[k] = (long long)part_base[s.u] + (long long)(blockIdx.x - cfirst[s.u]) * s.R + rr[k];
+          if constexpr (kTree)
+            prow[k] = (long long)(2 * blockIdx.x + (s.i0 == 0 ? 1 : 0)) * kMaxRows + rr[k];
+          else
+            prow[k] = (long long)part_base[s.u] + (long long)(blockIdx.x - cfirst[s.u]) * s.R + rr[k];
         }
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 64) {
@@ -952,10 +1033,10 @@ cudaError_t launch_verify_tc(const AttnParams& p, int rows_cap, int ncta, bool i
 #define SPLASH_TC(DD, SWA, IT)                                                                 \
   do {                                                                                         \
     constexpr int smem = tc::Cfg<DD>::kSmemBytes;                                              \
-    cudaError_t e = ensure_dynamic_smem<tc::verify_tc_kernel<DD, SWA, IT>>(smem);             \
+    cudaError_t e = ensure_dynamic_smem<tc::verify_tc_kernel<DD, SWA, IT, false>>(smem);      \
     if (e != cudaSuccess) return e;                                                            \
-    e = launch_dependent(tc::verify_tc_kernel<DD, SWA, IT>, dim3(ncta), dim3(tc::kThreads),    \
-                         smem, stream, p);                                                     \
+    e = launch_dependent(tc::verify_tc_kernel<DD, SWA, IT, false>, dim3(ncta),                 \
+                         dim3(tc::kThreads), smem, stream, p);                                 \
     if (e != cudaSuccess) return e;                                                            \
   } while (0)
   const bool swa = p.window > 0;
@@ -975,6 +1056,24 @@ cudaError_t launch_verify_tc(const AttnParams& p, int rows_cap, int ncta, bool i
   }
 #undef SPLASH_TC
   return cudaGetLastError();
+}
+
+cudaError_t launch_verify_tree(const TreeAttnParams& p, int ncta, cudaStream_t stream) {
+#define SPLASH_TREE(DD)                                                                        \
+  do {                                                                                         \
+    constexpr int smem = tc::Cfg<DD>::kSmemBytes;                                              \
+    constexpr auto kernel = tc::verify_tc_kernel<DD, false, false, true>;                      \
+    cudaError_t e = ensure_dynamic_smem<kernel>(smem);                                         \
+    if (e != cudaSuccess) return e;                                                            \
+    return launch_dependent(kernel, dim3(ncta), dim3(tc::kThreads), smem, stream, p);          \
+  } while (0)
+  switch (p.head_dim) {
+    case 64: SPLASH_TREE(64);
+    case 128: SPLASH_TREE(128);
+    case 256: SPLASH_TREE(256);
+    default: return cudaErrorNotSupported;
+  }
+#undef SPLASH_TREE
 }
 
 }  // namespace splash

@@ -20,6 +20,7 @@ DEVICE_BAD_PAGE = 1
 DEVICE_BAD_LENGTH = 2
 DEVICE_TIMEOUT = 3
 DEVICE_OUT_OF_PAGES = 5
+DEVICE_BAD_TREE = 6
 PATH_AUTO, PATH_SIMT, PATH_TENSOR, PATH_TENSOR_T = 0, 1, 2, 3
 # PATH_TENSOR: tensor-core kernel with the query rows on the MMA's M side (any
 # head_dim of 128 / 256, up to 128 rows); PATH_TENSOR_T: the transposed kernel
@@ -99,6 +100,20 @@ def _load() -> ctypes.CDLL:
     lib.splash_choose_targets.restype = I
     lib.splash_choose_targets.argtypes = [P, I, L, I, I, P, I, I, P, P, L, P, P, P, P, P, P, I, P,
                                           L, I, P, P, L, P, P, S, P, P]
+    lib.splash_tree_masks.restype = I
+    lib.splash_tree_masks.argtypes = [P, I, P, P, I, I, P, I, P, P, P, P]
+    lib.splash_verify_attention_tree_workspace_size.restype = S
+    lib.splash_verify_attention_tree_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.splash_verify_attention_tree.restype = I
+    lib.splash_verify_attention_tree.argtypes = attn[:10] + [P, I] + attn[10:] + [I]
+    lib.splash_accept_tree.restype = I
+    lib.splash_accept_tree.argtypes = [P, P, P, I, P, P, P, P, P, P, P, I, I, P, P]
+    lib.splash_kv_compact.restype = I
+    lib.splash_kv_compact.argtypes = [P, P, P, P, L, L, I, P, P, I, P, P, I, I, I, I, I, P, P]
+    lib.splash_token_logprobs_workspace_size.restype = S
+    lib.splash_token_logprobs_workspace_size.argtypes = [I, I]
+    lib.splash_token_logprobs.restype = I
+    lib.splash_token_logprobs.argtypes = [P, I, L, I, I, P, I, P, P, P, I, P, P, P, S, P, P]
     return lib
 
 
@@ -114,7 +129,10 @@ EXPORTED = ("splash_status_string", "splash_abi_version", "splash_tensor_path_su
             "splash_verify_attention_fixed_scratch_bytes", "splash_verify_attention_fixed_scratch",
             "splash_build_tables", "splash_build_tables_served", "splash_release_pages", "splash_qkv_append",
             "splash_kv_gather", "splash_token_state_stride", "splash_token_state_add",
-            "splash_choose_targets_workspace_size", "splash_choose_targets")
+            "splash_choose_targets_workspace_size", "splash_choose_targets", "splash_tree_masks",
+            "splash_verify_attention_tree_workspace_size", "splash_verify_attention_tree",
+            "splash_accept_tree", "splash_kv_compact", "splash_token_logprobs_workspace_size",
+            "splash_token_logprobs")
 
 
 def tensor_path_available(head_dim: int) -> bool:
@@ -158,15 +176,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def alloc_pool(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda"):
+def alloc_pool(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda",
+               num_layers: int = 0):
     """Zeroed paged pool in the library's layout: (k_pages, v_pages, k_scales,
     v_scales). The codes are one allocation [num_pages, Hkv, 2, P, D]; k_pages
     and v_pages are its [:, :, 0] and [:, :, 1] views ([num_pages, Hkv, P, D]
-    each, K and V codes of a (page, KV head) adjacent)."""
-    codes = torch.zeros((num_pages, num_kv_heads, 2, PAGE_SIZE, head_dim), dtype=torch.int8,
-                        device=device)
-    scales = (num_pages, num_kv_heads, PAGE_SIZE)
-    return (codes[:, :, 0], codes[:, :, 1],
+    each, K and V codes of a (page, KV head) adjacent). ``num_layers`` > 0: that
+    many pools in one allocation, each tensor with a leading layer axis (the form
+    that splash_kv_compact takes whole; index it for the calls of one layer)."""
+    layers = (num_layers,) if num_layers > 0 else ()
+    codes = torch.zeros((*layers, num_pages, num_kv_heads, 2, PAGE_SIZE, head_dim),
+                        dtype=torch.int8, device=device)
+    scales = (*layers, num_pages, num_kv_heads, PAGE_SIZE)
+    return (codes[..., 0, :, :], codes[..., 1, :, :],
             torch.zeros(scales, dtype=torch.float32, device=device),
             torch.zeros(scales, dtype=torch.float32, device=device))
 
@@ -672,3 +694,197 @@ def splash_choose_targets(logits, q_offsets, target_tokens, workspace, max_block
         _raw_stream(stream, dev))
     if st != 0:
         raise SplashError(st, "splash_choose_targets")
+
+
+# ---------------------------------------------------------------------------
+# Verification of a tree of drafts
+# ---------------------------------------------------------------------------
+def splash_tree_masks(parents, q_offsets, masks, max_block_len: int, context_lens=None,
+                      depths=None, positions=None, device_status=None, stream=None) -> None:
+    """Ancestor bits ``masks`` (int32 [n, >= ceil(max_block_len / 32)]), ``depths``
+    and ``positions`` (int32 [n]; the positions need ``context_lens``) of the nodes
+    of every tree."""
+    _tensors(parents=parents, q_offsets=q_offsets, masks=masks)
+    i32 = torch.int32
+    dev = _check_all(((parents, "parents", i32, 1), (q_offsets, "q_offsets", i32, 1),
+                      (masks, "masks", i32, 2), (context_lens, "context_lens", i32, 1),
+                      (depths, "depths", i32, 1), (positions, "positions", i32, 1)), device_status)
+    n, B = parents.shape[0], q_offsets.shape[0] - 1
+    if B < 0 or masks.shape[0] != n or (depths is not None and depths.shape[0] != n) \
+            or (positions is not None and positions.shape[0] != n) \
+            or (context_lens is not None and context_lens.shape[0] != B):
+        raise ValueError("shape mismatch between the parents, the offsets and the outputs")
+    if positions is not None and context_lens is None:
+        raise ValueError("positions need context_lens")
+    st = LIB.splash_tree_masks(parents.data_ptr(), n, q_offsets.data_ptr(), _data(context_lens), B,
+                               int(max_block_len), masks.data_ptr(), masks.shape[1],
+                               _data(depths), _data(positions), _data(device_status),
+                               _raw_stream(stream, dev))
+    if st != 0:
+        raise SplashError(st, "splash_tree_masks")
+
+
+def splash_verify_attention_tree_workspace_size(num_seqs: int, num_q_tokens: int, num_q_heads: int,
+                                                num_kv_heads: int, head_dim: int,
+                                                max_block_len: int, ctas: int = 0) -> int:
+    return int(LIB.splash_verify_attention_tree_workspace_size(
+        num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, max_block_len, ctas))
+
+
+def alloc_tree_workspace(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                         max_block_len, device="cuda", ctas: int = 0) -> torch.Tensor:
+    """Workspace for splash_verify_attention_tree."""
+    n = splash_verify_attention_tree_workspace_size(num_seqs, num_q_tokens, num_q_heads,
+                                                    num_kv_heads, head_dim, max_block_len, ctas)
+    if n == 0:
+        raise ValueError("invalid shape for the workspace size query")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def splash_verify_attention_tree(q, k_pages, v_pages, k_scales, v_scales, page_table,
+                                 context_lens, block_lens, tree_masks, sm_scale: float,
+                                 max_block_len: int, out, lse, workspace, device_status=None,
+                                 stream=None, ctas: int = 0) -> None:
+    """splash_verify_attention under the block masks ``tree_masks`` (int32
+    [n, words], as splash_tree_masks writes them). The workspace from
+    ``alloc_tree_workspace``."""
+    _tensors(q=q, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
+             page_table=page_table, context_lens=context_lens, block_lens=block_lens,
+             tree_masks=tree_masks, out=out, lse=lse, workspace=workspace)
+    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
+    dev = _check_all(((q, "q", b16, 3), (out, "out", b16, 3), (lse, "lse", f32, 2),
+                      (k_scales, "k_scales", f32, 3), (v_scales, "v_scales", f32, 3),
+                      (page_table, "page_table", i32, 2), (context_lens, "context_lens", i32, 1),
+                      (block_lens, "block_lens", i32, 1), (tree_masks, "tree_masks", i32, 2),
+                      (workspace, "workspace", torch.uint8, 1)), device_status)
+    pool = num_pages, hkv, P, D = _pool_on(k_pages, v_pages, dev)
+    n, hq, d = q.shape
+    B = context_lens.shape[0]
+    if d != D or P != PAGE_SIZE or out.shape != q.shape or lse.shape != (n, hq) \
+            or k_scales.shape != pool[:3] or v_scales.shape != pool[:3] \
+            or block_lens.shape[0] != B or page_table.shape[0] != B or tree_masks.shape[0] != n:
+        raise ValueError("shape mismatch between q, out, lse, the masks, the lengths and the pool")
+    st = LIB.splash_verify_attention_tree(
+        q.data_ptr(), n, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(),
+        block_lens.data_ptr(), tree_masks.data_ptr(), tree_masks.shape[1], B, hq, hkv, D, P,
+        num_pages, int(max_block_len), float(sm_scale), out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), workspace.shape[0], _data(device_status), _raw_stream(stream, dev),
+        int(ctas))
+    if st != 0:
+        raise SplashError(st, "splash_verify_attention_tree")
+
+
+def splash_accept_tree(block_tokens, parents, target_tokens, q_offsets, context_lens, accepted,
+                       next_tokens, path_rows, path_tokens, max_block_len: int,
+                       context_lens_out=None, device_status=None, stream=None) -> None:
+    """The accepted path through every tree: its rows and tokens (``path_tokens``
+    may be None), the accepted counts and next tokens. ``context_lens`` is advanced
+    in place unless ``context_lens_out`` is given."""
+    _tensors(block_tokens=block_tokens, parents=parents, target_tokens=target_tokens,
+             q_offsets=q_offsets, context_lens=context_lens, accepted=accepted,
+             next_tokens=next_tokens, path_rows=path_rows)
+    ctx_out = context_lens if context_lens_out is None else context_lens_out
+    i32 = torch.int32
+    dev = _check_all(((block_tokens, "block_tokens", i32, 1), (parents, "parents", i32, 1),
+                      (target_tokens, "target_tokens", i32, 1), (q_offsets, "q_offsets", i32, 1),
+                      (context_lens, "context_lens", i32, 1), (ctx_out, "context_lens_out", i32, 1),
+                      (accepted, "accepted", i32, 1), (next_tokens, "next_tokens", i32, 1),
+                      (path_rows, "path_rows", i32, 1), (path_tokens, "path_tokens", i32, 1)),
+                     device_status)
+    n, B = block_tokens.shape[0], context_lens.shape[0]
+    if parents.shape[0] != n or target_tokens.shape[0] != n or path_rows.shape[0] != n \
+            or (path_tokens is not None and path_tokens.shape[0] != n) \
+            or q_offsets.shape[0] != B + 1 or ctx_out.shape[0] != B or accepted.shape[0] != B \
+            or next_tokens.shape[0] != B:
+        raise ValueError("shape mismatch between the tokens, the offsets and the outputs")
+    st = LIB.splash_accept_tree(
+        block_tokens.data_ptr(), parents.data_ptr(), target_tokens.data_ptr(), n,
+        q_offsets.data_ptr(), context_lens.data_ptr(), ctx_out.data_ptr(), accepted.data_ptr(),
+        next_tokens.data_ptr(), path_rows.data_ptr(), _data(path_tokens), B, int(max_block_len),
+        _data(device_status), _raw_stream(stream, dev))
+    if st != 0:
+        raise SplashError(st, "splash_accept_tree")
+
+
+def splash_kv_compact(k_pages, v_pages, k_scales, v_scales, slots, path_rows, q_offsets, accepted,
+                      device_status=None, stream=None) -> None:
+    """The cache rows of the accepted nodes moved to the block's first slots, in one
+    pool or, with a leading layer axis on the pool's four tensors (``alloc_pool(...,
+    num_layers=L)``), in every layer's."""
+    _tensors(k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, slots=slots,
+             path_rows=path_rows, q_offsets=q_offsets, accepted=accepted)
+    f32, i32 = torch.float32, torch.int32
+    axes = k_pages.dim() - 1
+    dev = _check_all(((k_scales, "k_scales", f32, axes), (v_scales, "v_scales", f32, axes),
+                      (slots, "slots", i32, 1), (path_rows, "path_rows", i32, 1),
+                      (q_offsets, "q_offsets", i32, 1), (accepted, "accepted", i32, 1)),
+                     device_status)
+    layers, code_layer, scale_layer, k0, v0 = 1, 0, 0, k_pages, v_pages
+    if axes == 4:
+        layers = k_pages.shape[0]
+        if layers == 0 or v_pages.dim() != 5 or v_pages.shape[0] != layers \
+                or v_pages.stride(0) != k_pages.stride(0):
+            raise ValueError("k_pages and v_pages must be views of one pool per layer")
+        code_layer, scale_layer = k_pages.stride(0), k_scales.stride(0)
+        k0, v0 = k_pages[0], v_pages[0]
+    num_pages, hkv, P, D = _pool_on(k0, v0, dev)
+    n, B = slots.shape[0], accepted.shape[0]
+    if P != PAGE_SIZE or k_scales.shape != k_pages.shape[:-1] or v_scales.shape != k_scales.shape \
+            or path_rows.shape[0] != n or q_offsets.shape[0] != B + 1:
+        raise ValueError("shape mismatch between the slots, the path, the offsets and the pool")
+    st = LIB.splash_kv_compact(
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        code_layer, scale_layer, layers, slots.data_ptr(), path_rows.data_ptr(), n,
+        q_offsets.data_ptr(), accepted.data_ptr(), B, hkv, D, P, num_pages, _data(device_status),
+        _raw_stream(stream, dev))
+    if st != 0:
+        raise SplashError(st, "splash_kv_compact")
+
+
+def splash_token_logprobs_workspace_size(num_out: int, vocab: int) -> int:
+    return int(LIB.splash_token_logprobs_workspace_size(int(num_out), int(vocab)))
+
+
+def alloc_logprobs_workspace(num_out: int, vocab: int, device="cuda") -> torch.Tensor:
+    """Workspace for splash_token_logprobs of up to ``num_out`` rows."""
+    n = splash_token_logprobs_workspace_size(num_out, vocab)
+    if n == 0:
+        raise ValueError("invalid shape for the workspace size query")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def splash_token_logprobs(logits, workspace, tokens=None, logprobs=None, entropy=None,
+                          top_ids=None, top_logprobs=None, rows=None, device_status=None,
+                          stream=None) -> None:
+    """``logits``: float32, bfloat16 or float16 [n, vocab] with contiguous rows (a
+    view of wider rows is fine). Outputs have one entry a row, or one per entry of
+    ``rows`` (int32, -1: left as it was); ``tokens`` (int32 [n]) goes by the logits'
+    rows. ``top_ids`` / ``top_logprobs``: int32 / float32 [outputs, k], k <= 32."""
+    _tensors(logits=logits, workspace=workspace)
+    f32, i32 = torch.float32, torch.int32
+    dev = _check_all(((workspace, "workspace", torch.uint8, 1), (tokens, "tokens", i32, 1),
+                      (logprobs, "logprobs", f32, 1), (entropy, "entropy", f32, 1),
+                      (top_ids, "top_ids", i32, 2), (top_logprobs, "top_logprobs", f32, 2),
+                      (rows, "rows", i32, 1)), device_status)
+    dt = logits.dtype
+    if dt not in _DTYPES or logits.dim() != 2 or logits.get_device() != dev:
+        raise TypeError(f"logits must be a 2-D float32, bfloat16 or float16 tensor on cuda:{dev}")
+    n, vocab = logits.shape
+    if logits.stride(1) != 1 and vocab > 1:
+        raise ValueError("the rows of logits must be contiguous")
+    m = n if rows is None else rows.shape[0]
+    if (tokens is None) != (logprobs is None) or (top_ids is None) != (top_logprobs is None):
+        raise ValueError("tokens go with logprobs, top_ids with top_logprobs")
+    if tokens is not None and (tokens.shape[0] != n or logprobs.shape[0] != m) \
+            or entropy is not None and entropy.shape[0] != m \
+            or top_ids is not None and (top_ids.shape[0] != m
+                                        or top_logprobs.shape != top_ids.shape):
+        raise ValueError("shape mismatch between the rows and the outputs")
+    st = LIB.splash_token_logprobs(
+        logits.data_ptr(), _DTYPES[dt], max(logits.stride(0), vocab) if n < 2 else logits.stride(0),
+        n, vocab, _data(rows), m, _data(tokens), _data(logprobs), _data(entropy),
+        0 if top_ids is None else top_ids.shape[1], _data(top_ids), _data(top_logprobs),
+        workspace.data_ptr(), workspace.shape[0], _data(device_status), _raw_stream(stream, dev))
+    if st != 0:
+        raise SplashError(st, "splash_token_logprobs")
