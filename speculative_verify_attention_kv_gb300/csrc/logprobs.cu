@@ -16,8 +16,8 @@
 // pass has anyway: ordered by (maximum, lowest segment first), the k first segments
 // hold the k largest values by (value, lowest index first), since a value of another
 // segment has k values before it. Only those segments are read again, and of them
-// only what reaches the k-th segment's maximum is ordered. (A vocabulary of fewer
-// segments is read again whole, and the maxima of the threads' shares stand in for
+// only what reaches the k-th segment's maximum is ordered. (A vocabulary of no more than
+// k segments is read again whole, and the maxima of the threads' shares stand in for
 // the segments'.)
 //
 // Kernel 1: a warp per run of 512-value blocks of a row -> (m, S, W) and the segments'
@@ -30,12 +30,16 @@
 namespace splash {
 namespace {
 
-constexpr int kBlock = 512;              // values that a warp takes at a time
-constexpr int kMaxSegments = 512;        // of a row (and one more where it begins off 16 bytes)
+constexpr int kLoads = 4;                // 16-byte loads of a lane in a block
+constexpr int kRunBlocks = 8;            // of a run at most
+constexpr int kUnit = 256;               // values of the smallest segment
+constexpr int kSegsPerThread = 6;        // of the join: it holds a row's segments in registers
 constexpr int kMaxTop = 32;
 constexpr int kPassThreads = 256;
-constexpr int kJoinThreads = 128;
-constexpr int kCandidates = 1024;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kSelect = kThreads - 32;   // threads that hold segments
+constexpr int kMaxSegments = kSelect * kSegsPerThread;
+constexpr int kHot = 256, kCandidates = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kMaxFinite = 3.402823466e38f;
 constexpr float kMoveLog2 = 8.0f;
@@ -52,8 +56,7 @@ struct Params {
   int top;
   int32_t* top_ids;
   float* top_logprobs;
-  int blocks;                            // of a row at most
-  int seg_blocks;                        // blocks of a segment
+  int seg_units;                         // of a segment, a power of two
   int segments;                          // of a row at most
   int run_blocks, runs;                  // blocks of a run, runs of a row
   float* seg_max;                        // [num_out, segments]
@@ -81,26 +84,30 @@ __device__ inline float unordered(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
-// The types' 16-byte vectors: clamped to at least kLow (NaN and -inf too), as pairs of
-// fp32. A block whose maximum is above kFast holds nothing near kLow that counts: the
-// clamped values' exponentials are 0.
+// The types' 16-byte vectors as pairs of fp32, as they are or raised to a low finite
+// value (NaN and -inf too). In a block whose maximum is above kFast the exponentials of
+// raised values are 0. kBlock: values that a warp takes at a time.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int kPer = 4;
+  static constexpr int kPer = 4, kBlock = 32 * kLoads * kPer;
   static constexpr float kFast = -9e37f;
   static __device__ uint4 empty() {
     return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
   }
   static __device__ void put(uint4& v, int i, float x) { (&v.x)[i] = __float_as_uint(x); }
-  static __device__ float largest(const uint4& v) {
+  static __device__ float largest1(const uint4& v) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
                  fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
   static __device__ float2 pair(const uint4& v, int i) {
     const uint32_t a = i == 0 ? v.x : v.z, b = i == 0 ? v.y : v.w;
-    return make_float2(fmaxf(__uint_as_float(a), -1e38f), fmaxf(__uint_as_float(b), -1e38f));
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+  }
+  static __device__ float2 raised(const uint4& v, int i) {
+    const float2 f = pair(v, i);
+    return make_float2(fmaxf(f.x, -1e38f), fmaxf(f.y, -1e38f));
   }
   static __device__ float raw(const uint4& v, int i) {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
@@ -108,7 +115,7 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int kPer = 8;
+  static constexpr int kPer = 8, kBlock = 32 * kLoads * kPer;
   static constexpr float kFast = -9e37f;
   static __device__ uint4 empty() {
     return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
@@ -119,15 +126,20 @@ struct Vec<__nv_bfloat16> {
   static __device__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
   }
-  static __device__ float largest(const uint4& v) {
-    const __nv_bfloat162 m = __hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w)));
+  static __device__ __nv_bfloat162 largest2(const uint4& v) {
+    return __hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w)));
+  }
+  static __device__ float largest1(const uint4& v) {
+    const __nv_bfloat162 m = largest2(v);
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ float2 pair(const uint4& v, int i) {
-    const __nv_bfloat162 low = __floats2bfloat162_rn(-1e38f, -1e38f);
-    const __nv_bfloat162 c = __hmax2(as(word(v, i)), low);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(&c);
+  static __device__ float2 floats(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ float2 pair(const uint4& v, int i) { return floats(word(v, i)); }
+  static __device__ float2 raised(const uint4& v, int i) {
+    const __nv_bfloat162 c = __hmax2(as(word(v, i)), __floats2bfloat162_rn(-1e38f, -1e38f));
+    return floats(*reinterpret_cast<const uint32_t*>(&c));
   }
   static __device__ float raw(const uint4& v, int i) {
     const uint32_t w = word(v, i >> 1);
@@ -136,7 +148,7 @@ struct Vec<__nv_bfloat16> {
 };
 template <>
 struct Vec<__half> {
-  static constexpr int kPer = 8;
+  static constexpr int kPer = 8, kBlock = 32 * kLoads * kPer;
   static constexpr float kFast = -60000.f;
   static __device__ uint4 empty() {
     return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
@@ -145,11 +157,15 @@ struct Vec<__half> {
   static __device__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
   }
-  static __device__ float largest(const uint4& v) {
-    const __half2 m = __hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w)));
+  static __device__ __half2 largest2(const uint4& v) {
+    return __hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w)));
+  }
+  static __device__ float largest1(const uint4& v) {
+    const __half2 m = largest2(v);
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ float2 pair(const uint4& v, int i) {
+  static __device__ float2 pair(const uint4& v, int i) { return __half22float2(as(word(v, i))); }
+  static __device__ float2 raised(const uint4& v, int i) {
     return __half22float2(__hmax2(as(word(v, i)), __floats2half2_rn(-65504.f, -65504.f)));
   }
   static __device__ float raw(const uint4& v, int i) {
@@ -214,117 +230,206 @@ __device__ inline void move_reference(float m, float m2, float& S, float& W) {
   S *= f;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPassThreads) logprobs_pass_kernel(Params p) {
-  constexpr int kPer = Vec<T>::kPer, kLoads = kBlock / 32 / kPer;
-  allow_dependent_launch();
-  const int lane = threadIdx.x & 31;
-  const long long unit = ((long long)blockIdx.x * kPassThreads + threadIdx.x) >> 5;
-  const int i = (int)(unit / p.runs), run = (int)(unit % p.runs);
-  if (i >= p.num_out) return;
-  const int r = out_row(p, i);
-  if (r < 0) return;
-  const Row<T> row(p.logits, p.stride, r, p.vocab);
-  const int b0 = run * p.run_blocks;
-  const int b1 = min(b0 + p.run_blocks, (row.end + kBlock - 1) / kBlock);
-  float m = -INFINITY, seg = -INFINITY;
+// What a warp has summed: S and W as pairs that are added up at the end.
+struct Sums {
+  float m = -INFINITY;                   // the same in every lane
   float2 S = make_float2(0.f, 0.f), W = make_float2(0.f, 0.f);
-  float* seg_out = p.seg_max + (long long)i * p.segments + b0 / p.seg_blocks;
-  int left = p.seg_blocks;
-  uint4 v[kLoads];
+  __device__ void refer_to(float m2) {
+    float s = S.x + S.y, w = W.x + W.y;
+    move_reference(m, m2, s, w);
+    S = make_float2(s, 0.f);
+    W = make_float2(w, 0.f);
+    m = m2;
+  }
+};
+
+// A block value by value: the ends of a row, and values at the ends of the types'
+// range (infinity counts as the largest finite value). Returns the units' maxima.
+template <typename T>
+__device__ inline void block_by_value(const Row<T>& row, int b, Sums& a,
+                                      float (&unit)[Vec<T>::kBlock / kUnit]) {
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u) v[u] = row.load(b0 * kBlock + (32 * u + lane) * kPer);
-  for (int b = b0; b < b1; ++b) {
-    uint4 x[kLoads];
+  for (int g = 0; g < Vec<T>::kBlock / kUnit; ++g) {
+    const int p0 = b * Vec<T>::kBlock + g * kUnit + (threadIdx.x & 31);
+    float z[kUnit / 32], top = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      x[u] = v[u];
-      if (b + 1 < b1) v[u] = row.load((b + 1) * kBlock + (32 * u + lane) * kPer);
+    for (int u = 0; u < kUnit / 32; ++u) {
+      const int at = p0 + 32 * u;
+      z[u] = at >= row.shift && at < row.end ? (float)row.base[at] : -INFINITY;
+      top = fmaxf(top, z[u]);            // NaN is nothing
     }
-    float top = Vec<T>::largest(x[0]);
+    top = warp_fmax(top);
+    unit[g] = top;
+    if (top == -INFINITY) continue;
+    if (fminf(top, kMaxFinite) > a.m) a.refer_to(fminf(top, kMaxFinite));
 #pragma unroll
-    for (int u = 1; u < kLoads; ++u) top = fmaxf(top, Vec<T>::largest(x[u]));
-    top = warp_fmax(fmaxf(top, -INFINITY));        // NaN is nothing
-    seg = fmaxf(seg, top);
-    if (--left == 0 || b + 1 == b1) {
-      if (lane == 0) *seg_out = seg;
-      ++seg_out;
-      left = p.seg_blocks;
-      seg = -INFINITY;
+    for (int u = 0; u < kUnit / 32; ++u) {
+      if (!(z[u] > -INFINITY)) continue;           // NaN neither
+      const float t = fmaxf((fminf(z[u], kMaxFinite) - a.m) * kLog2e, -2000.f), e = ex2(t);
+      a.S.x += e;
+      a.W.x += e * t;
     }
-    if (top > Vec<T>::kFast && fmaxf(top, m) < 1e37f) {
-      if (!((top - m) * kLog2e <= kMoveLog2)) {
-        float s = S.x + S.y, w = W.x + W.y;
-        move_reference(m, top, s, w);
-        S = make_float2(s, 0.f);
-        W = make_float2(w, 0.f);
-        m = top;
+  }
+}
+
+// One warp over the blocks [b0, b1) of a row: its (m, S, W) in every lane, and the
+// maxima of the segments that it covers, the first of them to seg_out[0].
+template <typename T>
+__device__ inline float3 run_over(const Row<T>& row, int b0, int b1, int seg_units,
+                                  float* seg_out) {
+  constexpr int kPer = Vec<T>::kPer, kBlock = Vec<T>::kBlock;
+  constexpr int kUnits = kBlock / kUnit, kLoadsPerUnit = kLoads / kUnits;
+  const int lane = threadIdx.x & 31;
+  // the blocks that lie inside the row
+  const int in0 = min(max(b0, row.shift > 0 ? 1 : 0), b1), in1 = max(min(b1, row.end / kBlock), in0);
+  Sums a;
+  float seg = -INFINITY;
+  int left = seg_units / kUnits;         // blocks of the segment to come, where it has several
+  bool careful = false;                  // the same in every lane
+  const auto note = [&](const float (&unit)[kUnits], float top, bool last) {
+    if (seg_units >= kUnits) {
+      seg = fmaxf(seg, top);
+      if (--left <= 0 || last) {
+        if (lane == 0) *seg_out = seg;
+        ++seg_out;
+        left = seg_units / kUnits;
+        seg = -INFINITY;
       }
-      const float2 scale = make_float2(kLog2e, kLog2e), shift = make_float2(-m * kLog2e, -m * kLog2e);
+    } else {                             // a lane per segment
+      float mine = top;
+#pragma unroll
+      for (int g = 0; g < kUnits; ++g)
+        if (lane * seg_units == g) mine = seg_units == 1 ? unit[g] : fmaxf(unit[g], unit[g ^ 1]);
+      if (lane * seg_units < kUnits) seg_out[lane] = mine;
+      seg_out += kUnits / seg_units;
+    }
+  };
+  const auto edge = [&](int b) {
+    float unit[kUnits];
+    block_by_value(row, b, a, unit);
+    float top = unit[0];
+#pragma unroll
+    for (int g = 1; g < kUnits; ++g) top = fmaxf(top, unit[g]);
+    note(unit, top, b + 1 == b1);
+  };
+  uint4 v[kLoads], x[kLoads];
+  const uint4* from = reinterpret_cast<const uint4*>(row.base) + (long long)in0 * (kBlock / kPer) + lane;
+  const auto fetch = [&] {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) v[u] = __ldg(from + 32 * u);
+    from += kBlock / kPer;
+  };
+  if (in0 < in1) fetch();
+#pragma unroll 1
+  for (int b = b0; b < in0; ++b) edge(b);
+#pragma unroll 1
+  for (int b = in0; b < in1; ++b) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) x[u] = v[u];
+    if (b + 1 < in1) fetch();
+    float unit[kUnits];
+#pragma unroll
+    for (int g = 0; g < kUnits; ++g) {
+      float t = Vec<T>::largest1(x[g * kLoadsPerUnit]);
+#pragma unroll
+      for (int u = 1; u < kLoadsPerUnit; ++u)
+        t = fmaxf(t, Vec<T>::largest1(x[g * kLoadsPerUnit + u]));
+      unit[g] = warp_fmax(fmaxf(t, -INFINITY));    // NaN is nothing
+    }
+    float top = unit[0];
+#pragma unroll
+    for (int g = 1; g < kUnits; ++g) top = fmaxf(top, unit[g]);
+    note(unit, top, b + 1 == b1);
+    if (!(top > Vec<T>::kFast && fmaxf(top, a.m) < 1e37f)) {
+      if (top > -INFINITY) block_by_value(row, b, a, unit);
+      continue;
+    }
+    if (!((top - a.m) * kLog2e <= kMoveLog2)) a.refer_to(top);
+    const float2 scale = make_float2(kLog2e, kLog2e);
+    const float2 shift = make_float2(-a.m * kLog2e, -a.m * kLog2e);
+    if (!careful) {
+      const float2 S0 = a.S, W0 = a.W;
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
 #pragma unroll
         for (int k = 0; k < kPer / 2; ++k) {
           const float2 t = __ffma2_rn(Vec<T>::pair(x[u], k), scale, shift);
           const float2 e = make_float2(ex2(t.x), ex2(t.y));
-          S = __fadd2_rn(S, e);
-          W = __ffma2_rn(e, t, W);
+          a.S = __fadd2_rn(a.S, e);
+          a.W = __ffma2_rn(e, t, a.W);
         }
-    } else if (top > -INFINITY) {
-      // values at the ends of the types' range, infinity as the largest finite one
-      const float lim = fminf(top, kMaxFinite);
-      if (lim > m) {
-        float s = S.x + S.y, w = W.x + W.y;
-        move_reference(m, lim, s, w);
-        S = make_float2(s, 0.f);
-        W = make_float2(w, 0.f);
-        m = lim;
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const float z = Vec<T>::raw(x[u], k);
-          if (!(z > -INFINITY)) continue;          // NaN neither
-          const float t = fmaxf((fminf(z, kMaxFinite) - m) * kLog2e, -2000.f), e = ex2(t);
-          S.x += e;
-          W.x += e * t;
-        }
+      // a value of -inf (or near it, or NaN) has made W NaN: this block again, and
+      // the rest of the run, with such values raised
+      careful = __any_sync(0xffffffffu, !(a.W.x + a.W.y == a.W.x + a.W.y));
+      if (!careful) continue;
+      a.S = S0;
+      a.W = W0;
     }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k) {
+        const float2 t = __ffma2_rn(Vec<T>::raised(x[u], k), scale, shift);
+        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+        a.S = __fadd2_rn(a.S, e);
+        a.W = __ffma2_rn(e, t, a.W);
+      }
   }
-  const float s = warp_sum(S.x + S.y), w = warp_sum(W.x + W.y);
-  if (lane == 0) p.part[(long long)i * p.runs + run] = make_float4(m, s, w, 0.f);
+#pragma unroll 1
+  for (int b = in1; b < b1; ++b) edge(b);
+  return make_float3(a.m, warp_sum(a.S.x + a.S.y), warp_sum(a.W.x + a.W.y));
 }
 
+// Adds a run to (m, S, W).
+__device__ inline void add_run(float& m, float& S, float& W, float m2, float S2, float W2) {
+  if (m2 > m) {
+    move_reference(m, m2, S, W);
+    m = m2;
+  } else {
+    move_reference(m2, m, S2, W2);
+  }
+  S += S2;
+  W += W2;
+}
+
+struct JoinSmem {
+  uint32_t bound[kSelect / 32];
+  int maxima, hot, count;
+  int segs[kMaxTop];
+  float least, m, lns;
+  unsigned long long max_key[kMaxSegments];        // maximum and segment
+  int hot_place[kHot];
+  unsigned long long key[kCandidates], best[kWarps];
+};
+
+// How many of v[0 .. n) are larger.
+__device__ inline int rank_of(const unsigned long long* v, int n, unsigned long long mine) {
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) rank += v[j] > mine;
+  return rank;
+}
+
+// A CTA per row: a chain of short steps, each with a warp to a scheduler or less, so that
+// it costs what the steps have in instructions (4 to 5 cycles each) and round trips.
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
   constexpr int kPer = Vec<T>::kPer;
-  constexpr int kSegsPerLane = (kMaxSegments + 32) / 32;
-  __shared__ int s_segs[kMaxTop];
-  __shared__ float s_least;
-  __shared__ int s_count;
-  __shared__ float s_m, s_lns;
-  __shared__ uint32_t s_own[kJoinThreads];
-  __shared__ unsigned long long s_key[kCandidates];
-  __shared__ unsigned long long s_best[kJoinThreads / 32];
+  __shared__ JoinSmem s;
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
   const int r = out_row(p, i);
   if (r < 0) return;
   const Row<T> row(p.logits, p.stride, r, p.vocab);
-  if (warp == 0) {
-    const int runs = ((row.end + kBlock - 1) / kBlock + p.run_blocks - 1) / p.run_blocks;
+  const int n = (row.end + p.seg_units * kUnit - 1) / (p.seg_units * kUnit);   // segments
+  if (warp == kWarps - 1) {
+    // the row's runs
+    const int blocks = (row.end + Vec<T>::kBlock - 1) / Vec<T>::kBlock;
+    const int runs = (blocks + p.run_blocks - 1) / p.run_blocks;
     float m = -INFINITY, S = 0.f, W = 0.f;
     for (int j = lane; j < runs; j += 32) {
-      float4 q = p.part[(long long)i * p.runs + j];
-      if (q.x > m) {
-        move_reference(m, q.x, S, W);
-        m = q.x;
-      } else {
-        move_reference(q.x, m, q.y, q.z);
-      }
-      S += q.y;
-      W += q.z;
+      const float4 q = p.part[(long long)i * p.runs + j];
+      add_run(m, S, W, q.x, q.y, q.z);
     }
     const float all = warp_max(m);
     move_reference(m, all, S, W);
@@ -332,8 +437,8 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(Params p) {
     W = warp_sum(W);
     if (lane == 0) {
       const float lns = logf(S);                   // S is 0 or at least about 2^-8
-      s_m = all;
-      s_lns = lns;
+      s.m = all;
+      s.lns = lns;
       if (p.entropy) p.entropy[i] = S > 0.f ? fmaxf(lns - kLn2 * (W / S), 0.f) : 0.f;
       if (p.tokens) {
         const int tok = p.tokens[r];
@@ -342,97 +447,123 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(Params p) {
         p.logprobs[i] = z > -INFINITY ? (fminf(z, kMaxFinite) - all) - lns : -INFINITY;
       }
     }
-  } else if (warp == 1 && p.top > 0) {
-    // the segments of the `top` largest maxima, the lowest first among equal ones
-    const int n = ((row.end + kBlock - 1) / kBlock + p.seg_blocks - 1) / p.seg_blocks;
-    uint32_t key[kSegsPerLane];
-#pragma unroll
-    for (int u = 0; u < kSegsPerLane; ++u) {
-      const int j = 32 * u + lane;
-      key[u] = j < n ? ordered(p.seg_max[(long long)i * p.segments + j]) : 0u;
-    }
-    uint32_t last = 0;
-    int found = 0;
-    for (; found < p.top; ++found) {
-      uint32_t mine = 0;
-#pragma unroll
-      for (int u = 0; u < kSegsPerLane; ++u) mine = max(mine, key[u]);
-      const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
-      if (best == 0) break;                        // no segment is left
-      int at = INT_MAX;
-#pragma unroll
-      for (int u = kSegsPerLane - 1; u >= 0; --u)
-        if (key[u] == best) at = 32 * u + lane;
-      const int j = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-      for (int u = 0; u < kSegsPerLane; ++u)
-        if (32 * u + lane == j) key[u] = 0u;
-      if (lane == 0) s_segs[found] = j;
-      last = best;
-    }
-    if (lane == 0) {
-      s_count = 0;
-      s_least = unordered(last);
-      for (int u = found; u < p.top; ++u) s_segs[u] = -1;
-    }
   }
   if (p.top == 0) return;
+  // The segments of the `top` largest maxima, the lowest first among equal ones. First a
+  // bound that so many reach: of each warp, what a share of its lanes reach.
+  uint32_t key[kSegsPerThread] = {}, mine = 0;
+  if (warp < kWarps - 1) {
+#pragma unroll
+    for (int u = 0; u < kSegsPerThread; ++u) {
+      const int j = kSelect * u + tid;
+      if (j < n) key[u] = ordered(p.seg_max[(long long)i * p.segments + j]);
+    }
+#pragma unroll
+    for (int u = 0; u < kSegsPerThread; ++u) mine = max(mine, key[u]);
+    uint32_t reached = 0;
+#pragma unroll 1
+    for (int u = 0; u < p.top; u += kWarps - 1) {
+      reached = __reduce_max_sync(0xffffffffu, mine);
+      if (mine == reached) mine = 0;
+    }
+    if (lane == 0) s.bound[warp] = reached;
+  }
+  if (tid < kMaxTop) s.segs[tid] = -1;
+  if (tid == 0) {
+    s.maxima = s.hot = s.count = 0;
+    s.least = -INFINITY;
+  }
   __syncthreads();
-  const int seg_vecs = p.seg_blocks * (kBlock / kPer);
+  const uint32_t bound = max(min(min(s.bound[0], s.bound[1]), s.bound[2]), 1u);
+  static_assert(kWarps == 4, "bounds of three warps");
+#pragma unroll
+  for (int u = 0; u < kSegsPerThread; ++u)
+    if (key[u] >= bound)                           // (a place without a segment is 0)
+      s.max_key[atomicAdd(&s.maxima, 1)] =
+          (unsigned long long)key[u] << 32 | (uint32_t)~(kSelect * u + tid);
+  __syncthreads();
+  for (int c = tid; c < s.maxima; c += kThreads) {
+    const unsigned long long k = s.max_key[c];
+    const int rank = rank_of(s.max_key, s.maxima, k);
+    if (rank < p.top) s.segs[rank] = (int)~(uint32_t)k;
+    if (rank == p.top - 1 && n > p.top) s.least = unordered((uint32_t)(k >> 32));
+  }
+  __syncthreads();
+  const int seg_vecs = p.seg_units * (kUnit / kPer);
   const int vecs = p.top * seg_vecs;
   const auto place_of = [&](int v) {
-    const int s = s_segs[v / seg_vecs];
-    return s < 0 ? INT_MAX : s * (p.seg_blocks * kBlock) + v % seg_vecs * kPer;
+    const int g = s.segs[v / seg_vecs];
+    return g < 0 ? INT_MAX : g * (p.seg_units * kUnit) + v % seg_vecs * kPer;
   };
   const auto key_of = [&](float z, int place) {
     return (unsigned long long)ordered(z) << 32 | (uint32_t)~(place - row.shift);
   };
-  if (s_segs[p.top - 1] < 0) {
-    // fewer segments than that: the threads' own values take their place
+  if (n <= p.top) {
+    // no more segments than that: the threads' own values take their place
     float mine = -INFINITY;
-    for (int v = tid; v < vecs; v += kJoinThreads) {
+    for (int v = tid; v < vecs; v += kThreads) {
       const int p0 = place_of(v);
-      if (p0 < row.end) mine = fmaxf(mine, Vec<T>::largest(row.load(p0)));
+      if (p0 < row.end) mine = fmaxf(mine, Vec<T>::largest1(row.load(p0)));
     }
-    s_own[tid] = ordered(mine);
+    s.key[tid] = (unsigned long long)ordered(mine) << 32 | (uint32_t)~tid;
     __syncthreads();
-    int rank = 0;
-    for (int j = 0; j < kJoinThreads; ++j)
-      rank += s_own[j] > s_own[tid] || (s_own[j] == s_own[tid] && j < tid);
-    if (rank == p.top - 1) s_least = mine;
+    if (rank_of(s.key, kThreads, s.key[tid]) == p.top - 1) s.least = mine;
     __syncthreads();
   }
-  // what reaches the last of those maxima
-  const float least = s_least;
-  for (int v = tid; v < vecs; v += kJoinThreads) {
-    const int p0 = place_of(v);
-    if (p0 >= row.end) continue;
-    const uint4 x = row.load(p0);
-    if (!(Vec<T>::largest(x) >= least)) continue;
+  // vectors with a value that reaches the last of those maxima: a warp per segment,
+  // kBatch vectors on their way
+  const float least = s.least;
+  constexpr int kBatch = sizeof(T) == 4 ? 10 : 5;            // for 20 segments
+  const int per_seg = seg_vecs / 32, steps = (p.top + kWarps - 1 - warp) / kWarps * per_seg;
+  for (int s0 = 0; s0 < steps; s0 += kBatch) {
+    uint4 x[kBatch];
+    int at[kBatch];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const float z = Vec<T>::raw(x, k);
-      if (z >= least && z > -INFINITY) {
-        const int c = atomicAdd(&s_count, 1);
-        if (c < kCandidates) s_key[c] = key_of(z, p0 + k);
-      }
+    for (int u = 0; u < kBatch; ++u) {
+      const int st = s0 + u, q = per_seg == 1 ? st : per_seg == 2 ? st >> 1 : st / per_seg;
+      const int g = st < steps ? s.segs[warp + kWarps * q] : -1;
+      at[u] = g * (p.seg_units * kUnit) + (32 * (st - q * per_seg) + lane) * kPer;
+      const bool whole = g >= 0 && at[u] >= row.shift && at[u] + kPer <= row.end;
+      x[u] = Vec<T>::empty();
+      if (whole) x[u] = __ldg(reinterpret_cast<const uint4*>(row.base + at[u]));
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (Vec<T>::largest1(x[u]) >= fmaxf(least, -kMaxFinite)) {
+        const int c = atomicAdd(&s.hot, 1);
+        if (c < kHot) s.hot_place[c] = at[u];
+      }
   }
   __syncthreads();
-  const int count = s_count;
-  const auto put = [&](int rank, unsigned long long key) {
-    const float z = fminf(unordered((uint32_t)(key >> 32)), kMaxFinite);
-    p.top_ids[(long long)i * p.top + rank] = (int32_t)~(uint32_t)key;
-    p.top_logprobs[(long long)i * p.top + rank] = (z - s_m) - s_lns;
+  // their values, and those of the row's ends (which may lie in other segments)
+  const auto offer = [&](int place) {
+    const float z = (float)row.base[place];
+    if (!(z >= least && z > -INFINITY)) return;
+    const int c = atomicAdd(&s.count, 1);
+    if (c < kCandidates) s.key[c] = key_of(z, place);
   };
-  if (count <= kCandidates) {
-    for (int c = tid; c < count; c += kJoinThreads) {
-      const unsigned long long key = s_key[c];
-      int rank = 0;
-      for (int j = 0; j < count; ++j) rank += s_key[j] > key;
-      if (rank < p.top) put(rank, key);
+  const int hot = s.hot;
+  for (int e = tid; e < min(hot, kHot) * kPer; e += kThreads)
+    offer(s.hot_place[e / kPer] + e % kPer);
+  if (tid < kPer) {
+    if (row.shift > 0 && tid >= row.shift && tid < row.end) offer(tid);
+    const int place = row.end / kPer * kPer + tid;         // of the last vector, if cut
+    if (place < row.end && (place >= kPer || row.shift == 0)) offer(place);
+  }
+  __syncthreads();
+  const int count = s.count;
+  const auto put = [&](int rank, unsigned long long k) {
+    const float z = fminf(unordered((uint32_t)(k >> 32)), kMaxFinite);
+    p.top_ids[(long long)i * p.top + rank] = (int32_t)~(uint32_t)k;
+    p.top_logprobs[(long long)i * p.top + rank] = (z - s.m) - s.lns;
+  };
+  if (hot <= kHot && count <= kCandidates) {
+    for (int c = tid; c < count; c += kThreads) {
+      const unsigned long long k = s.key[c];
+      const int rank = rank_of(s.key, count, k);
+      if (rank < p.top) put(rank, k);
     }
-    for (int c = count + tid; c < p.top; c += kJoinThreads) {
+    for (int c = count + tid; c < p.top; c += kThreads) {
       p.top_ids[(long long)i * p.top + c] = -1;
       p.top_logprobs[(long long)i * p.top + c] = -INFINITY;
     }
@@ -442,7 +573,7 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(Params p) {
   unsigned long long below = ~0ull;
   for (int rank = 0; rank < p.top; ++rank) {
     unsigned long long best = 0;
-    for (int v = tid; v < vecs; v += kJoinThreads) {
+    for (int v = tid; v < vecs; v += kThreads) {
       const int p0 = place_of(v);
       if (p0 >= row.end) continue;
       const uint4 x = row.load(p0);
@@ -458,38 +589,73 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(Params p) {
       const unsigned long long y = __shfl_xor_sync(0xffffffffu, best, o);
       best = y > best ? y : best;
     }
-    if (lane == 0) s_best[warp] = best;
+    if (lane == 0) s.best[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) best = s_best[w] > best ? s_best[w] : best;
+    for (int w = 0; w < kWarps; ++w) best = s.best[w] > best ? s.best[w] : best;
     __syncthreads();
     if (tid == 0) put(rank, best);
     below = best;
   }
 }
 
+// A warp per run.
+template <typename T>
+__global__ void __launch_bounds__(kPassThreads, 4) logprobs_pass_kernel(Params p) {
+  allow_dependent_launch();
+  const unsigned unit = blockIdx.x * (kPassThreads / 32) + (threadIdx.x >> 5);
+  const int i = unit / (unsigned)p.runs, run = unit - i * p.runs;
+  if (i >= p.num_out) return;
+  const int r = out_row(p, i);
+  if (r < 0) return;
+  const Row<T> row(p.logits, p.stride, r, p.vocab);
+  const int blocks = (row.end + Vec<T>::kBlock - 1) / Vec<T>::kBlock;
+  const int b0 = run * p.run_blocks, b1 = min(b0 + p.run_blocks, blocks);
+  const long long seg0 = (long long)i * p.segments + b0 * (Vec<T>::kBlock / kUnit) / p.seg_units;
+  const float3 q = run_over<T>(row, b0, b1, p.seg_units, p.seg_max + seg0);
+  if ((threadIdx.x & 31) == 0)
+    p.part[(long long)i * p.runs + run] = make_float4(q.x, q.y, q.z, 0.f);
+}
+
+// Segments of a row (which may begin off 16 bytes): units, doubled until a warp's
+// registers hold their maxima. With room for those that only a last block's rest has.
 struct Shape {
-  int blocks, seg_blocks, segments;
+  int units, seg_units, segments;
 };
 Shape shape_of(int vocab) {
   Shape s;
-  s.blocks = (vocab + 7 + kBlock - 1) / kBlock;      // a row may begin off 16 bytes
-  s.seg_blocks = (s.blocks + kMaxSegments - 1) / kMaxSegments;
-  s.segments = (s.blocks + s.seg_blocks - 1) / s.seg_blocks;
+  s.units = (vocab + 7 + kUnit - 1) / kUnit;
+  s.seg_units = 1;
+  while ((s.units + s.seg_units - 1) / s.seg_units > kMaxSegments) s.seg_units *= 2;
+  s.segments = (s.units + s.seg_units - 1) / s.seg_units + 3;
   return s;
 }
 size_t seg_bytes(const Shape& s, int num_out) {
   return ((size_t)num_out * s.segments * sizeof(float) + 15) & ~size_t(15);
 }
+int up(long long a, long long b) { return (int)((a + b - 1) / b * b); }
 
 template <typename T>
-int launch(const Params& p, cudaStream_t s) {
-  const long long warps = (long long)p.num_out * p.runs;
-  const long long grid = (warps * 32 + kPassThreads - 1) / kPassThreads;
-  if (grid > INT_MAX) return SPLASH_ERR_INVALID_ARGUMENT;
+int launch(Params& p, void* workspace, int sms, cudaStream_t s) {
+  const Shape sh = shape_of(p.vocab);
+  constexpr int kUnits = Vec<T>::kBlock / kUnit;
+  p.seg_units = sh.seg_units;
+  p.segments = sh.segments;
+  // runs of whole segments, about one for each of 32 warps an SM, and no longer than
+  // that leaves the last of them short
+  const int blocks = (sh.units + kUnits - 1) / kUnits;
+  const long long per = ((long long)p.num_out * blocks + 32LL * sms - 1) / (32LL * sms);
+  p.run_blocks = up(per < kRunBlocks ? per : kRunBlocks,
+                    sh.seg_units > kUnits ? sh.seg_units / kUnits : 1);
+  p.runs = (blocks + p.run_blocks - 1) / p.run_blocks;
+  p.seg_max = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + seg_bytes(sh, p.num_out));
+  constexpr int kWarpsPerCta = kPassThreads / 32;
+  const long long grid = ((long long)p.num_out * p.runs + kWarpsPerCta - 1) / kWarpsPerCta;
+  if (grid * kWarpsPerCta > INT_MAX) return SPLASH_ERR_INVALID_ARGUMENT;
   logprobs_pass_kernel<T><<<(int)grid, kPassThreads, 0, s>>>(p);
   if (counted(cudaGetLastError()) != cudaSuccess) return SPLASH_ERR_CUDA;
-  return counted(launch_dependent(logprobs_join_kernel<T>, dim3(p.num_out), dim3(kJoinThreads), 0,
-                                  s, p)) == cudaSuccess
+  return counted(launch_dependent(logprobs_join_kernel<T>, dim3(p.num_out), dim3(kThreads), 0, s,
+                                  p)) == cudaSuccess
              ? SPLASH_OK
              : SPLASH_ERR_CUDA;
 }
@@ -503,8 +669,9 @@ extern "C" {
 
 size_t splash_token_logprobs_workspace_size(int num_out, int vocab) {
   if (num_out <= 0 || vocab <= 0 || vocab > (1 << 30)) return 0;
+  // a run has at least a block, 512 values of the widest type
   const Shape s = shape_of(vocab);
-  return seg_bytes(s, num_out) + (size_t)num_out * s.blocks * sizeof(float4);
+  return seg_bytes(s, num_out) + (size_t)num_out * ((s.units + 1) / 2) * sizeof(float4);
 }
 
 int splash_token_logprobs(const void* logits, int dtype, long long logits_stride, int num_rows,
@@ -526,13 +693,6 @@ int splash_token_logprobs(const void* logits, int dtype, long long logits_stride
     return SPLASH_ERR_WORKSPACE_TOO_SMALL;
   const int sms = device_sm_count();
   if (sms <= 0) return SPLASH_ERR_CUDA;
-  const Shape sh = shape_of(vocab);
-  // runs: about a run for every resident warp, of whole segments; long ones where the
-  // rows alone fill the GPU, since a run ends with a reduction over the warp
-  const long long all = (long long)num_out * sh.blocks;
-  long long per = (all + 32LL * sms - 1) / (32LL * sms);
-  per = per < 1 ? 1 : per > 32 ? 32 : per;
-  per = (per + sh.seg_blocks - 1) / sh.seg_blocks * sh.seg_blocks;
   Params p;
   p.logits = logits;
   p.stride = logits_stride;
@@ -546,19 +706,12 @@ int splash_token_logprobs(const void* logits, int dtype, long long logits_stride
   p.top = top;
   p.top_ids = top_ids;
   p.top_logprobs = top_logprobs;
-  p.blocks = sh.blocks;
-  p.seg_blocks = sh.seg_blocks;
-  p.segments = sh.segments;
-  p.run_blocks = (int)per;
-  p.runs = (sh.blocks + p.run_blocks - 1) / p.run_blocks;
-  p.seg_max = static_cast<float*>(workspace);
-  p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + seg_bytes(sh, num_out));
   p.status = device_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case SPLASH_F32: return launch<float>(p, s);
-    case SPLASH_BF16: return launch<__nv_bfloat16>(p, s);
-    default: return launch<__half>(p, s);
+    case SPLASH_F32: return launch<float>(p, workspace, sms, s);
+    case SPLASH_BF16: return launch<__nv_bfloat16>(p, workspace, sms, s);
+    default: return launch<__half>(p, workspace, sms, s);
   }
 }
 
