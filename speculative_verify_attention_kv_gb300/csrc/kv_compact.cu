@@ -35,7 +35,7 @@ struct CompactParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_compact_kernel(CompactParams p) {
+__global__ void __launch_bounds__(kThreads, 8) kv_compact_kernel(CompactParams p) {
   constexpr int kPieces = 2 * D / 16;            // of a row, K and V
   constexpr int kRows = 32 / kPieces;            // rows of one load of the warp
   const int lane = threadIdx.x & 31;
@@ -43,12 +43,8 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(CompactParams p) {
   if (unit >= (long long)p.num_seqs * p.num_layers * p.hkv) return;
   const int h = (int)(unit % p.hkv), bl = (int)(unit / p.hkv);
   const int l = bl % p.num_layers, b = bl / p.num_layers;
-  const int first = p.q_offsets[b], end = p.q_offsets[b + 1], count = p.accepted[b] + 1;
-  if (count <= 1) return;                        // the root is where it belongs
-  if (first < 0 || end > p.num_tokens || count > end - first) {
-    if (lane == 0) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
-    return;
-  }
+  const int first = p.q_offsets[b], end = p.q_offsets[b + 1];
+  const bool usable = first >= 0 && first <= end && end <= p.num_tokens;
   int8_t* codes = p.codes + l * p.code_layer;
   float* ks = p.k_scales + l * p.scale_layer;
   float* vs = p.v_scales + l * p.scale_layer;
@@ -56,17 +52,30 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(CompactParams p) {
   // pieces of the K row, then of the V row, kPageSize rows further on
   const int off = (piece / (D / 16)) * kPageSize * D + (piece % (D / 16)) * 16;
 
+  // a lane per row: where it comes from and goes to (read beside the count, not after it)
+  int from = -1, dst = -1;
+  if (usable && 1 + lane < end - first) {
+    from = p.path_rows[first + 1 + lane];
+    dst = p.slots[first + 1 + lane];
+  }
+  const int count = p.accepted[b] + 1;
+  if (count <= 1) return;                        // the root is where it belongs
+  if (!usable || count > end - first) {
+    if (lane == 0) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
+    return;
+  }
   for (int base = 1; base < count; base += 32) {
-    // a lane per row: where it comes from and goes to
     const int i = base + lane;
-    int src = -1, dst = -1;
+    if (base > 1 && i < count) {
+      from = p.path_rows[first + i];
+      dst = p.slots[first + i];
+    }
+    int src = -1;
     if (i < count) {
-      const int from = p.path_rows[first + i];
       if (from < first + i || from >= end) {
         report(p.status, SPLASH_DEVICE_BAD_TREE);
       } else if (from != first + i) {
         src = p.slots[from];
-        dst = p.slots[first + i];
         if (src >= p.num_pages * kPageSize || dst >= p.num_pages * kPageSize) {
           report(p.status, SPLASH_DEVICE_BAD_PAGE);
           src = -1;

@@ -697,8 +697,40 @@ def splash_choose_targets(logits, q_offsets, target_tokens, workspace, max_block
 
 
 # ---------------------------------------------------------------------------
-# Verification of a tree of drafts
+# Verification of a tree of drafts. A step's small calls are bound by their host
+# time, most of it these checks: one pass that asks each tensor for its type,
+# device, shape and layout, and the wording apart.
 # ---------------------------------------------------------------------------
+def _check_shapes(required, optional, device_status) -> int:
+    """required, optional: (tensor, name, dtype, shape) of contiguous tensors on the
+    current device, the optional ones possibly None. Returns the device index."""
+    dev = torch.cuda.current_device()
+    try:
+        for t, _, dtype, shape in required:
+            if t.dtype is not dtype or t.get_device() != dev or t.shape != shape \
+                    or not t.is_contiguous():
+                break
+        else:
+            for t, _, dtype, shape in optional:
+                if t is not None and (t.dtype is not dtype or t.get_device() != dev
+                                      or t.shape != shape or not t.is_contiguous()):
+                    break
+            else:
+                if device_status is None:
+                    return dev
+    except AttributeError:
+        pass
+    for t, name, _, _ in required:               # the same with words
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    both = (*required, *optional)
+    _check_all([(t, name, dtype, None) for t, name, dtype, _ in both], device_status)
+    for t, name, _, shape in both:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return dev
+
+
 def splash_tree_masks(parents, q_offsets, masks, max_block_len: int, context_lens=None,
                       depths=None, positions=None, device_status=None, stream=None) -> None:
     """Ancestor bits ``masks`` (int32 [n, >= ceil(max_block_len / 32)]), ``depths``
@@ -706,18 +738,18 @@ def splash_tree_masks(parents, q_offsets, masks, max_block_len: int, context_len
     of every tree."""
     _tensors(parents=parents, q_offsets=q_offsets, masks=masks)
     i32 = torch.int32
-    dev = _check_all(((parents, "parents", i32, 1), (q_offsets, "q_offsets", i32, 1),
-                      (masks, "masks", i32, 2), (context_lens, "context_lens", i32, 1),
-                      (depths, "depths", i32, 1), (positions, "positions", i32, 1)), device_status)
-    n, B = parents.shape[0], q_offsets.shape[0] - 1
-    if B < 0 or masks.shape[0] != n or (depths is not None and depths.shape[0] != n) \
-            or (positions is not None and positions.shape[0] != n) \
-            or (context_lens is not None and context_lens.shape[0] != B):
-        raise ValueError("shape mismatch between the parents, the offsets and the outputs")
+    n, B = parents.numel(), q_offsets.numel() - 1
+    words = masks.shape[-1]
+    dev = _check_shapes(((parents, "parents", i32, (n,)), (q_offsets, "q_offsets", i32, (B + 1,)),
+                         (masks, "masks", i32, (n, words))),
+                        ((context_lens, "context_lens", i32, (B,)), (depths, "depths", i32, (n,)),
+                         (positions, "positions", i32, (n,))), device_status)
+    if B < 0:
+        raise ValueError("q_offsets has num_seqs + 1 entries")
     if positions is not None and context_lens is None:
         raise ValueError("positions need context_lens")
     st = LIB.splash_tree_masks(parents.data_ptr(), n, q_offsets.data_ptr(), _data(context_lens), B,
-                               int(max_block_len), masks.data_ptr(), masks.shape[1],
+                               int(max_block_len), masks.data_ptr(), words,
                                _data(depths), _data(positions), _data(device_status),
                                _raw_stream(stream, dev))
     if st != 0:
@@ -748,28 +780,32 @@ def splash_verify_attention_tree(q, k_pages, v_pages, k_scales, v_scales, page_t
     """splash_verify_attention under the block masks ``tree_masks`` (int32
     [n, words], as splash_tree_masks writes them). The workspace from
     ``alloc_tree_workspace``."""
-    _tensors(q=q, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
-             page_table=page_table, context_lens=context_lens, block_lens=block_lens,
-             tree_masks=tree_masks, out=out, lse=lse, workspace=workspace)
+    _tensors(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+             context_lens=context_lens, tree_masks=tree_masks, workspace=workspace)
     f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
-    dev = _check_all(((q, "q", b16, 3), (out, "out", b16, 3), (lse, "lse", f32, 2),
-                      (k_scales, "k_scales", f32, 3), (v_scales, "v_scales", f32, 3),
-                      (page_table, "page_table", i32, 2), (context_lens, "context_lens", i32, 1),
-                      (block_lens, "block_lens", i32, 1), (tree_masks, "tree_masks", i32, 2),
-                      (workspace, "workspace", torch.uint8, 1)), device_status)
-    pool = num_pages, hkv, P, D = _pool_on(k_pages, v_pages, dev)
-    n, hq, d = q.shape
-    B = context_lens.shape[0]
-    if d != D or P != PAGE_SIZE or out.shape != q.shape or lse.shape != (n, hq) \
-            or k_scales.shape != pool[:3] or v_scales.shape != pool[:3] \
-            or block_lens.shape[0] != B or page_table.shape[0] != B or tree_masks.shape[0] != n:
-        raise ValueError("shape mismatch between q, out, lse, the masks, the lengths and the pool")
+    if q.dim() != 3 or page_table.dim() != 2 or tree_masks.dim() != 2 or k_pages.dim() != 4:
+        raise ValueError("q has 3 dims, page_table and tree_masks 2, the pages 4")
+    n, hq, d = qs = q.shape
+    B, max_pages = context_lens.numel(), page_table.shape[1]
+    words, room = tree_masks.shape[1], workspace.numel()
+    num_pages, hkv, P, D = pool = k_pages.shape
+    dev = _check_shapes(((q, "q", b16, qs), (out, "out", b16, qs), (lse, "lse", f32, (n, hq)),
+                         (k_scales, "k_scales", f32, pool[:3]),
+                         (v_scales, "v_scales", f32, pool[:3]),
+                         (page_table, "page_table", i32, (B, max_pages)),
+                         (context_lens, "context_lens", i32, (B,)),
+                         (block_lens, "block_lens", i32, (B,)),
+                         (tree_masks, "tree_masks", i32, (n, words)),
+                         (workspace, "workspace", torch.uint8, (room,))), (), device_status)
+    _pool_on(k_pages, v_pages, dev)
+    if d != D or P != PAGE_SIZE:
+        raise ValueError("shape mismatch between q and the pool")
     st = LIB.splash_verify_attention_tree(
         q.data_ptr(), n, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-        v_scales.data_ptr(), page_table.data_ptr(), page_table.shape[1], context_lens.data_ptr(),
-        block_lens.data_ptr(), tree_masks.data_ptr(), tree_masks.shape[1], B, hq, hkv, D, P,
+        v_scales.data_ptr(), page_table.data_ptr(), max_pages, context_lens.data_ptr(),
+        block_lens.data_ptr(), tree_masks.data_ptr(), words, B, hq, hkv, D, P,
         num_pages, int(max_block_len), float(sm_scale), out.data_ptr(), lse.data_ptr(),
-        workspace.data_ptr(), workspace.shape[0], _data(device_status), _raw_stream(stream, dev),
+        workspace.data_ptr(), room, _data(device_status), _raw_stream(stream, dev),
         int(ctas))
     if st != 0:
         raise SplashError(st, "splash_verify_attention_tree")
@@ -781,23 +817,20 @@ def splash_accept_tree(block_tokens, parents, target_tokens, q_offsets, context_
     """The accepted path through every tree: its rows and tokens (``path_tokens``
     may be None), the accepted counts and next tokens. ``context_lens`` is advanced
     in place unless ``context_lens_out`` is given."""
-    _tensors(block_tokens=block_tokens, parents=parents, target_tokens=target_tokens,
-             q_offsets=q_offsets, context_lens=context_lens, accepted=accepted,
-             next_tokens=next_tokens, path_rows=path_rows)
+    _tensors(block_tokens=block_tokens, context_lens=context_lens)
     ctx_out = context_lens if context_lens_out is None else context_lens_out
     i32 = torch.int32
-    dev = _check_all(((block_tokens, "block_tokens", i32, 1), (parents, "parents", i32, 1),
-                      (target_tokens, "target_tokens", i32, 1), (q_offsets, "q_offsets", i32, 1),
-                      (context_lens, "context_lens", i32, 1), (ctx_out, "context_lens_out", i32, 1),
-                      (accepted, "accepted", i32, 1), (next_tokens, "next_tokens", i32, 1),
-                      (path_rows, "path_rows", i32, 1), (path_tokens, "path_tokens", i32, 1)),
-                     device_status)
-    n, B = block_tokens.shape[0], context_lens.shape[0]
-    if parents.shape[0] != n or target_tokens.shape[0] != n or path_rows.shape[0] != n \
-            or (path_tokens is not None and path_tokens.shape[0] != n) \
-            or q_offsets.shape[0] != B + 1 or ctx_out.shape[0] != B or accepted.shape[0] != B \
-            or next_tokens.shape[0] != B:
-        raise ValueError("shape mismatch between the tokens, the offsets and the outputs")
+    n, B = block_tokens.numel(), context_lens.numel()
+    rows, seqs = (n,), (B,)
+    dev = _check_shapes(((block_tokens, "block_tokens", i32, rows), (parents, "parents", i32, rows),
+                         (target_tokens, "target_tokens", i32, rows),
+                         (q_offsets, "q_offsets", i32, (B + 1,)),
+                         (context_lens, "context_lens", i32, seqs),
+                         (ctx_out, "context_lens_out", i32, seqs),
+                         (accepted, "accepted", i32, seqs),
+                         (next_tokens, "next_tokens", i32, seqs),
+                         (path_rows, "path_rows", i32, rows)),
+                        ((path_tokens, "path_tokens", i32, rows),), device_status)
     st = LIB.splash_accept_tree(
         block_tokens.data_ptr(), parents.data_ptr(), target_tokens.data_ptr(), n,
         q_offsets.data_ptr(), context_lens.data_ptr(), ctx_out.data_ptr(), accepted.data_ptr(),
@@ -812,27 +845,31 @@ def splash_kv_compact(k_pages, v_pages, k_scales, v_scales, slots, path_rows, q_
     """The cache rows of the accepted nodes moved to the block's first slots, in one
     pool or, with a leading layer axis on the pool's four tensors (``alloc_pool(...,
     num_layers=L)``), in every layer's."""
-    _tensors(k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, slots=slots,
-             path_rows=path_rows, q_offsets=q_offsets, accepted=accepted)
+    _tensors(k_pages=k_pages, v_pages=v_pages, slots=slots, accepted=accepted)
     f32, i32 = torch.float32, torch.int32
-    axes = k_pages.dim() - 1
-    dev = _check_all(((k_scales, "k_scales", f32, axes), (v_scales, "v_scales", f32, axes),
-                      (slots, "slots", i32, 1), (path_rows, "path_rows", i32, 1),
-                      (q_offsets, "q_offsets", i32, 1), (accepted, "accepted", i32, 1)),
-                     device_status)
-    layers, code_layer, scale_layer, k0, v0 = 1, 0, 0, k_pages, v_pages
-    if axes == 4:
-        layers = k_pages.shape[0]
-        if layers == 0 or v_pages.dim() != 5 or v_pages.shape[0] != layers \
-                or v_pages.stride(0) != k_pages.stride(0):
-            raise ValueError("k_pages and v_pages must be views of one pool per layer")
-        code_layer, scale_layer = k_pages.stride(0), k_scales.stride(0)
-        k0, v0 = k_pages[0], v_pages[0]
-    num_pages, hkv, P, D = _pool_on(k0, v0, dev)
-    n, B = slots.shape[0], accepted.shape[0]
-    if P != PAGE_SIZE or k_scales.shape != k_pages.shape[:-1] or v_scales.shape != k_scales.shape \
-            or path_rows.shape[0] != n or q_offsets.shape[0] != B + 1:
-        raise ValueError("shape mismatch between the slots, the path, the offsets and the pool")
+    shape, strides = k_pages.shape, k_pages.stride()
+    n, B = slots.numel(), accepted.numel()
+    dev = _check_shapes(((k_scales, "k_scales", f32, shape[:-1]),
+                         (v_scales, "v_scales", f32, shape[:-1]), (slots, "slots", i32, (n,)),
+                         (path_rows, "path_rows", i32, (n,)),
+                         (q_offsets, "q_offsets", i32, (B + 1,)),
+                         (accepted, "accepted", i32, (B,))), (), device_status)
+    layers, code_layer, scale_layer = 1, 0, 0
+    if len(shape) == 5:
+        layers, code_layer = shape[0], strides[0]
+        num_pages, hkv, P, D = shape[1:]
+        scale_layer = num_pages * hkv * P
+        if layers == 0 or v_pages.shape != shape or v_pages.stride() != strides \
+                or k_pages.dtype is not torch.int8 or v_pages.dtype is not torch.int8 \
+                or strides[1:] != (hkv * 2 * P * D, 2 * P * D, D, 1) \
+                or v_pages.data_ptr() != k_pages.data_ptr() + P * D \
+                or k_pages.get_device() != dev:
+            raise ValueError("k_pages and v_pages must be the halves of one pool per layer (see "
+                             "alloc_pool) on the current device")
+    else:
+        num_pages, hkv, P, D = _pool_on(k_pages, v_pages, dev)
+    if P != PAGE_SIZE:
+        raise ValueError(f"pages of {PAGE_SIZE} slots, not {P}")
     st = LIB.splash_kv_compact(
         k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
         code_layer, scale_layer, layers, slots.data_ptr(), path_rows.data_ptr(), n,
@@ -863,28 +900,33 @@ def splash_token_logprobs(logits, workspace, tokens=None, logprobs=None, entropy
     rows. ``top_ids`` / ``top_logprobs``: int32 / float32 [outputs, k], k <= 32."""
     _tensors(logits=logits, workspace=workspace)
     f32, i32 = torch.float32, torch.int32
-    dev = _check_all(((workspace, "workspace", torch.uint8, 1), (tokens, "tokens", i32, 1),
-                      (logprobs, "logprobs", f32, 1), (entropy, "entropy", f32, 1),
-                      (top_ids, "top_ids", i32, 2), (top_logprobs, "top_logprobs", f32, 2),
-                      (rows, "rows", i32, 1)), device_status)
     dt = logits.dtype
-    if dt not in _DTYPES or logits.dim() != 2 or logits.get_device() != dev:
-        raise TypeError(f"logits must be a 2-D float32, bfloat16 or float16 tensor on cuda:{dev}")
-    n, vocab = logits.shape
-    if logits.stride(1) != 1 and vocab > 1:
-        raise ValueError("the rows of logits must be contiguous")
-    m = n if rows is None else rows.shape[0]
+    if dt not in _DTYPES or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D float32, bfloat16 or float16 tensor")
     if (tokens is None) != (logprobs is None) or (top_ids is None) != (top_logprobs is None):
         raise ValueError("tokens go with logprobs, top_ids with top_logprobs")
-    if tokens is not None and (tokens.shape[0] != n or logprobs.shape[0] != m) \
-            or entropy is not None and entropy.shape[0] != m \
-            or top_ids is not None and (top_ids.shape[0] != m
-                                        or top_logprobs.shape != top_ids.shape):
-        raise ValueError("shape mismatch between the rows and the outputs")
+    if rows is not None:
+        _tensors(rows=rows)
+    if top_ids is not None:
+        _tensors(top_ids=top_ids)
+    n, vocab = logits.shape
+    m = n if rows is None else rows.numel()
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    room = workspace.numel()
+    dev = _check_shapes(((workspace, "workspace", torch.uint8, (room,)),),
+                        ((tokens, "tokens", i32, (n,)), (logprobs, "logprobs", f32, (m,)),
+                         (entropy, "entropy", f32, (m,)), (top_ids, "top_ids", i32, (m, top)),
+                         (top_logprobs, "top_logprobs", f32, (m, top)),
+                         (rows, "rows", i32, (m,))), device_status)
+    if logits.get_device() != dev:
+        raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
+    pitch, step = logits.stride()
+    if step != 1 and vocab > 1:
+        raise ValueError("the rows of logits must be contiguous")
     st = LIB.splash_token_logprobs(
-        logits.data_ptr(), _DTYPES[dt], max(logits.stride(0), vocab) if n < 2 else logits.stride(0),
+        logits.data_ptr(), _DTYPES[dt], max(pitch, vocab) if n < 2 else pitch,
         n, vocab, _data(rows), m, _data(tokens), _data(logprobs), _data(entropy),
-        0 if top_ids is None else top_ids.shape[1], _data(top_ids), _data(top_logprobs),
-        workspace.data_ptr(), workspace.shape[0], _data(device_status), _raw_stream(stream, dev))
+        top, _data(top_ids), _data(top_logprobs),
+        workspace.data_ptr(), room, _data(device_status), _raw_stream(stream, dev))
     if st != 0:
         raise SplashError(st, "splash_token_logprobs")
