@@ -59,6 +59,7 @@
 // in the last tiles, the nodes whose bits their masks have: a thread takes the 16
 // bits of its keys from the mask words, once per row and tile, and nothing else
 // of the softmax differs. Only the tiles that hold nodes (5 at most) pay for it.
+// The cut of the stream over the CTAs is computed here, by every CTA for itself.
 #include <type_traits>
 
 #include "splash_groups.cuh"
@@ -185,57 +186,59 @@ struct ItemSegIter {
 };
 
 // The same over sequences whose rows are cut into row blocks: units are
-// (sequence, KV head, row block), the blocks of a head next to each other.
+// (sequence, KV head, row block), the blocks of a head next to each other. A walk
+// from the CTA's first tile; the lengths are read again for every segment (they are
+// in the first-level cache), so that four numbers are all that a warp keeps of it.
+static_assert(kTreeTile == kTileKeys, "the plan's tiles");
 struct TreeSegIter {
-  const int* stp;
-  const int* seq_T;
-  const int* seq_ctx;
-  const int* q_off;
-  int B, G, Hkv;
-  int t, t_end;
+  const TreeAttnParams& p;
+  TreeStart at;
   __device__ bool next(Seg& s) {
-    if (t >= t_end) return false;
-    s.b = upper_index(stp, B - 1, t);
-    s.T = seq_T[s.b];
-    s.ctx = seq_ctx[s.b];
-    s.qbase = q_off[s.b];
-    s.Lk = s.ctx + s.T;
-    s.klo = 0;
-    const RowBlocks rb = row_blocks(s.T, G);
-    const int tiles = (s.Lk + kTileKeys - 1) / kTileKeys;
-    const int local = t - stp[s.b];
-    const int unit = local / tiles;
-    s.h = unit / rb.count;
-    s.r0 = (unit - s.h * rb.count) * rb.rows;
-    s.R = min(rb.rows, s.T * G - s.r0);
-    s.i0 = local - unit * tiles;
-    s.i1 = min(tiles, s.i0 + (t_end - t));
-    s.whole = s.i0 == 0 && s.i1 == tiles;
-    s.u = 0;
-    t += s.i1 - s.i0;
-    return true;
+    for (; at.count > 0 && at.b < p.num_seqs; ++at.b) {
+      const TreeSeq q(__ldg(p.block_lens + at.b), __ldg(p.context_lens + at.b), p.group,
+                      p.max_block_len, p.max_pages_per_seq);
+      if (q.T > 0 && at.local < p.num_kv_heads * q.rb.count * q.tiles) {
+        const int unit = at.local / q.tiles;
+        s.b = at.b;
+        s.T = q.T;
+        s.ctx = q.ctx;
+        s.qbase = at.q_off;
+        s.Lk = q.ctx + q.T;
+        s.klo = 0;
+        s.h = unit / q.rb.count;
+        s.r0 = (unit - s.h * q.rb.count) * q.rb.rows;
+        s.R = min(q.rb.rows, q.T * p.group - s.r0);
+        s.i0 = at.local - unit * q.tiles;
+        s.i1 = min(q.tiles, s.i0 + at.count);
+        s.whole = s.i0 == 0 && s.i1 == q.tiles;
+        s.u = 0;
+        at.local += s.i1 - s.i0;
+        at.count -= s.i1 - s.i0;
+        return true;
+      }
+      at.q_off += q.laid;
+      at.local = 0;
+    }
+    return false;
   }
 };
 
 // The plan's workspace layout: the plain one, or the one of a plan with
-// prefix groups or of trees (the same names for the regions the kernel reads).
-template <bool kItems, bool kTree>
-__device__ __forceinline__ auto layout_for(int B, int Hkv, int D, long long rows_bound) {
-  if constexpr (kTree)
-    return make_tree_layout(B, D, rows_bound);
-  else if constexpr (kItems)
+// prefix groups (the same names for the regions the kernel reads).
+template <bool kItems>
+__device__ __forceinline__ typename std::conditional<kItems, GroupLayout, WorkspaceLayout>::type
+layout_for(int B, int Hkv, int D, long long rows_bound) {
+  if constexpr (kItems)
     return make_group_layout(B, Hkv, D, rows_bound);
   else
     return make_layout(B, Hkv, D, rows_bound);
 }
 
-template <bool kItems, bool kTree>
-__device__ __forceinline__ auto make_iter(const int* stp, const int* seq_T, const int* seq_ctx,
-                                          const int* q_off, const ItemDesc* items, int B, int G,
-                                          int Hkv, int window, int t, int t_end) {
-  if constexpr (kTree)
-    return TreeSegIter{stp, seq_T, seq_ctx, q_off, B, G, Hkv, t, t_end};
-  else if constexpr (kItems)
+template <bool kItems>
+__device__ __forceinline__ typename std::conditional<kItems, ItemSegIter, SegIter>::type
+make_iter(const int* stp, const int* seq_T, const int* seq_ctx, const ItemDesc* items, int B,
+          int G, int Hkv, int window, int t, int t_end) {
+  if constexpr (kItems)
     return ItemSegIter{stp, items, max_items(B), G, Hkv, t, t_end};
   else
     return SegIter{stp, seq_T, seq_ctx, B, G, Hkv, window, t, t_end};
@@ -472,22 +475,24 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   // the set-up above overlaps the planner; from here on the plan is read
   grid_dependency_wait();
   const PlanHeader* hd = reinterpret_cast<const PlanHeader*>(p.ws);
-  if ((int)blockIdx.x >= hd->ncta[kClassTensor]) {         // no tiles for this CTA
+  TreeStart tree_at{0, 0, 0, 0};
+  bool idle;
+  if constexpr (kTree) idle = !tree_start(p, kbuf, tree_at);
+  else idle = (int)blockIdx.x >= hd->ncta[kClassTensor];
+  if (idle) {                                              // no tiles for this CTA
     if (warp == kMmaWarp)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                    "r"(kTmemCols) : "memory");
     return;
   }
   const int B = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
-  const auto L = layout_for<kItems, kTree>(B, Hkv, D, hd->rows_bound);
-  const int* q_off = reinterpret_cast<const int*>(p.ws + L.q_off);
-  const int* seq_T = reinterpret_cast<const int*>(p.ws + L.seq_T);
-  const int* seq_ctx = reinterpret_cast<const int*>(p.ws + L.seq_ctx);
-  const ItemDesc* items = static_cast<const ItemDesc*>(nullptr);
-  if constexpr (kItems) items = reinterpret_cast<const ItemDesc*>(p.ws + L.items);
-  const int* stp = reinterpret_cast<const int*>(p.ws + L.stp) + kClassTensor * (B + 1);
-  const int *nseg = nullptr, *cfirst = nullptr, *part_base = nullptr;
+  const auto L = [&] {
+    if constexpr (kTree) return make_tree_layout(B, D, tree_rows_bound(gridDim.x));
+    else return layout_for<kItems>(B, Hkv, D, hd->rows_bound);
+  }();
+  const int *q_off = nullptr, *nseg = nullptr, *cfirst = nullptr, *part_base = nullptr;
   if constexpr (!kTree) {
+    q_off = reinterpret_cast<const int*>(p.ws + L.q_off);
     nseg = reinterpret_cast<const int*>(p.ws + L.nseg);
     cfirst = reinterpret_cast<const int*>(p.ws + L.cfirst);
     part_base = reinterpret_cast<const int*>(p.ws + L.part_base);
@@ -496,9 +501,21 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   float* lse_part = reinterpret_cast<float*>(p.ws + L.lse_part);
 
   const int window = kSwa ? p.window : 0;
-  const int* cst = reinterpret_cast<const int*>(p.ws + L.cta_start) + kClassTensor * (kMaxCtas + 1);
-  auto iter = make_iter<kItems, kTree>(stp, seq_T, seq_ctx, q_off, items, B, G, Hkv, window,
-                                       cst[blockIdx.x], cst[blockIdx.x + 1]);
+  auto iter = [&] {
+    if constexpr (kTree) {
+      return TreeSegIter{p, tree_at};
+    } else {
+      const int* seq_T = reinterpret_cast<const int*>(p.ws + L.seq_T);
+      const int* seq_ctx = reinterpret_cast<const int*>(p.ws + L.seq_ctx);
+      const ItemDesc* items = static_cast<const ItemDesc*>(nullptr);
+      if constexpr (kItems) items = reinterpret_cast<const ItemDesc*>(p.ws + L.items);
+      const int* stp = reinterpret_cast<const int*>(p.ws + L.stp) + kClassTensor * (B + 1);
+      const int* cst =
+          reinterpret_cast<const int*>(p.ws + L.cta_start) + kClassTensor * (kMaxCtas + 1);
+      return make_iter<kItems>(stp, seq_T, seq_ctx, items, B, G, Hkv, window, cst[blockIdx.x],
+                               cst[blockIdx.x + 1]);
+    }
+  }();
 
   if (warp < kSoftmaxWarps) {
     // ===================================================== softmax + epilogue
@@ -1058,14 +1075,20 @@ cudaError_t launch_verify_tc(const AttnParams& p, int rows_cap, int ncta, bool i
   return cudaGetLastError();
 }
 
-cudaError_t launch_verify_tree(const TreeAttnParams& p, int ncta, cudaStream_t stream) {
+// `planned`: a planner runs before it on the stream (batches past kTreeSelfPlan).
+cudaError_t launch_verify_tree(const TreeAttnParams& p, int ncta, bool planned,
+                               cudaStream_t stream) {
 #define SPLASH_TREE(DD)                                                                        \
   do {                                                                                         \
     constexpr int smem = tc::Cfg<DD>::kSmemBytes;                                              \
     constexpr auto kernel = tc::verify_tc_kernel<DD, false, false, true>;                      \
     cudaError_t e = ensure_dynamic_smem<kernel>(smem);                                         \
     if (e != cudaSuccess) return e;                                                            \
-    return launch_dependent(kernel, dim3(ncta), dim3(tc::kThreads), smem, stream, p);          \
+    static_assert(kTreePlanRoom <= 2 * tc::Cfg<DD>::kTileBytes * tc::kStages, "plan's room");  \
+    if (planned)                                                                               \
+      return launch_dependent(kernel, dim3(ncta), dim3(tc::kThreads), smem, stream, p);        \
+    kernel<<<ncta, tc::kThreads, smem, stream>>>(p);                                           \
+    return cudaGetLastError();                                                                 \
   } while (0)
   switch (p.head_dim) {
     case 64: SPLASH_TREE(64);
