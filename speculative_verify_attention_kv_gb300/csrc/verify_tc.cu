@@ -527,6 +527,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     int g = 0, nsegs = 0;
     Seg s;
     bool ok = true;
+    uint32_t sst = 0, sc_phase = 0;                       // trees: tile g % kScStages, (g / kScStages) & 1
     while (ok && iter.next(s)) {
       // Q' of this segment overwrites the previous one: both QK issuers must
       // have seen the previous q_full phase (so neither lags it by two phases)
@@ -635,6 +636,167 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       warp_arrive(smem_u32(&sh->q_full), lane);
 
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // l: this thread's columns
+      if constexpr (kTree) {
+        // A softmax warp takes its tiles one after the
+        // other, and with 2 of them a scheduler it is their latency that bounds the kernel
+        // (2230 of the 2270 cycles of a tile at D = 64; 64, 128 and 256 took 241, 245 and
+        // 297 us for the same keys). So the chain of a tile is kept short: the running
+        // maximum is looked at by each thread for its own keys, and only where one passes
+        // it by more than 2^8 is it reduced over the row and moved, with O and the sums
+        // (the same decisions as a reduction every tile would take).
+        float base[2] = {0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // base: rowfac * (running maximum); limit: the x that moves it
+        float limit[2] = {-INFINITY, -INFINITY};
+        for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
+          const int st = g % kStages;
+          ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1));
+          if (!ok) break;                                   // a timeout seen by some lanes
+          fence_after();
+          if (warp_live) {
+            uint32_t pw[16];                                // P: 32 packed columns
+            uint32_t sv[32];
+            tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
+            // the scales' barrier and the K scales while the TMEM load is in flight
+            ok = sync.wait(smem_u32(&sh->sc_full[sst]), sc_phase);
+            const int k0 = it * kTileKeys;
+            const float* ks = scales + sst * 2 * kTileKeys;
+            const float* vs = ks + kTileKeys;
+            float2 ks2[8], x[2][8];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
+              ks2[2 * i4] = make_float2(kq.x, kq.y);
+              ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
+            }
+            tmem_wait_ld(sv);         // sv is read only after the wait
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                x[k][i] = __fmul2_rn(make_float2(__uint_as_float(sv[4 * i + 2 * k]),
+                                                 __uint_as_float(sv[4 * i + 2 * k + 1])), ks2[i]);
+            // which of this thread's keys (16 * quad + 2i + {0,1}) the rows see
+            uint32_t vm[2] = {0xffffu, 0xffffu};
+            bool full = true;
+            if (k0 + kTileKeys > s.ctx) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (rr[k] >= 0) {
+                  const int row = s.qbase + (s.r0 + rr[k]) / G;
+                  vm[k] = tree_bits16(p.tree_masks + (size_t)row * p.mask_stride,
+                                      k0 + 16 * quad - s.ctx, s.T);
+                }
+                full = full && vm[k] == 0xffffu;
+              }
+              if (!full) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    if (!(vm[k] >> (2 * i) & 1)) x[k][i].x = -INFINITY;
+                    if (!(vm[k] >> (2 * i + 1) & 1)) x[k][i].y = -INFINITY;
+                  }
+              }
+            }
+            float mt[2], alpha[2] = {1.f, 1.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              mt[k] = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) mt[k] = fmax3(mt[k], x[k][i].x, x[k][i].y);
+            }
+            if (__any_sync(0xffffffffu, mt[0] > limit[0] || (k1_live && mt[1] > limit[1]))) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float t = mt[k];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                if (t > limit[k]) {                          // the same in the row's threads
+                  alpha[k] = limit[k] == -INFINITY ? 0.f : ex2(base[k] - rowfac[k] * t);
+                  base[k] = rowfac[k] * t;
+                  limit[k] = t + kRescaleLog2 / rowfac[k];
+                  sum[k] = make_float2(sum[k].x * alpha[k], sum[k].y * alpha[k]);
+                }
+              }
+            }
+            float2 vs2[8];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const float4 vq4 = *reinterpret_cast<const float4*>(vs + 16 * quad + 4 * (i4 ^ quad));
+              vs2[2 * i4] = make_float2(vq4.x, vq4.y);
+              vs2[2 * i4 + 1] = make_float2(vq4.z, vq4.w);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (k == 1 && !k1_live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) pw[2 * i + 1] = 0u;
+                break;
+              }
+              const float2 rf2 = make_float2(rowfac[k], rowfac[k]);
+              const float2 nb2 = make_float2(-base[k], -base[k]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float2 vq = vs2[i];
+                if (!full) {      // scales of masked keys are not trusted
+                  if (!(vm[k] >> (2 * i) & 1)) vq.x = 0.f;
+                  if (!(vm[k] >> (2 * i + 1) & 1)) vq.y = 0.f;
+                }
+                const float2 e0 = __ffma2_rn(x[k][i], rf2, nb2);
+                const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
+                sum[k] = __fadd2_rn(sum[k], p0);
+                __half2 h0 = __float22half2_rn(__fmul2_rn(p0, vq));
+                pw[2 * i + k] = *reinterpret_cast<uint32_t*>(&h0);   // packed column 4i + quad
+              }
+            }
+            // O follows once the previous tile's PV is done (the first tile's PV does
+            // not add to O). p_free of that tile's buffer: its previous phase (PV three
+            // tiles back) is complete, so a parity wait cannot be satisfied by an older one.
+            if (it > s.i0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+              ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->p_free[(g - 1) % kStages]),
+                                                     ((g - 1) / kStages) & 1));
+              if (!ok) break;
+              fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 64) {
+                uint32_t v[32];
+                tmem_ld16x256_x8(tmem + lane_base + C::kOCol + c0, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    v[4 * i + 2 * k] = __float_as_uint(__uint_as_float(v[4 * i + 2 * k]) * alpha[k]);
+                    v[4 * i + 2 * k + 1] =
+                        __float_as_uint(__uint_as_float(v[4 * i + 2 * k + 1]) * alpha[k]);
+                  }
+                tmem_st16x256_x8(tmem + lane_base + C::kOCol + c0, v);
+              }
+            }
+            tmem_st16x128_x8(tmem + lane_base + C::kSCol + st * kTileKeys, pw);
+            tmem_wait_st();
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sh->p_full[st]));
+            mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
+          }
+          if (++sst == kScStages) sst = 0, sc_phase ^= 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          m[k] = base[k];                                 // rowfac * m
+          l[k] = sum[k].x + sum[k].y;
+          // the row again, from what was kept of it
+          live[k] = rr[k] >= 0;
+          const int j = s.r0 + max(rr[k], 0), tt = j / G;
+          qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + (j - tt * G);
+        }
+      } else {
       for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
         const int st = g % kStages, sst = g % kScStages;
         ok = sync.wait(smem_u32(&sh->sc_full[sst]), (g / kScStages) & 1) &&
@@ -673,23 +835,12 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           }
           // tile keys jj with nlo <= jj < nvis are visible to the row
           int nvis[2] = {kTileKeys, kTileKeys}, nlo[2] = {-1, -1};
-          uint32_t vm[2] = {0xffffu, 0xffffu};          // trees: which of this thread's keys
           bool full = true;
           // a tile below the block's keys (and, with a window, above every
           // row's lower bound) is visible to every row: no per-row bounds
           const bool tile_inside = k0 + kTileKeys <= s.ctx &&
                                    (!kSwa || s.ctx + s.T - window <= k0);
-          if constexpr (kTree) {
-            if (!tile_inside) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                if (live[k])
-                  vm[k] = tree_bits16(p.tree_masks + (size_t)lim[k] * p.mask_stride,
-                                      k0 + 16 * quad - s.ctx, s.T);
-                full = full && vm[k] == 0xffffu;
-              }
-            }
-          } else if (!tile_inside) {
+          if (!tile_inside) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               nvis[k] = live[k] ? min(kTileKeys, lim[k] - k0 + 1) : 0;
@@ -705,10 +856,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int j = 16 * quad + 2 * i;
-                if (kTree ? !(vm[k] >> (2 * i) & 1) : (j >= nvis[k] || j < nlo[k]))
-                  x[k][i].x = -INFINITY;
-                if (kTree ? !(vm[k] >> (2 * i + 1) & 1) : (j + 1 >= nvis[k] || j + 1 < nlo[k]))
-                  x[k][i].y = -INFINITY;
+                if (j >= nvis[k] || j < nlo[k]) x[k][i].x = -INFINITY;
+                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) x[k][i].y = -INFINITY;
               }
           }
           float base[2] = {0.f, 0.f};
@@ -762,9 +911,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
               float2 vq = vs2[i];
               if (!full) {      // scales of masked keys are not trusted
                 const int j = 16 * quad + 2 * i;
-                if (kTree ? !(vm[k] >> (2 * i) & 1) : (j >= nvis[k] || j < nlo[k])) vq.x = 0.f;
-                if (kTree ? !(vm[k] >> (2 * i + 1) & 1) : (j + 1 >= nvis[k] || j + 1 < nlo[k]))
-                  vq.y = 0.f;
+                if (j >= nvis[k] || j < nlo[k]) vq.x = 0.f;
+                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) vq.y = 0.f;
               }
               const float2 e0 = __ffma2_rn(x[k][i], rf2, nb2);
               const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
@@ -808,6 +956,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         }
         fence_before();
         warp_arrive(smem_u32(&sh->p_full[st]), lane);
+      }
       }
       if (!ok) break;
       // epilogue: last PV of the segment complete -> normalise, write out
@@ -860,7 +1009,9 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         for (int k = 0; k < 2; ++k) {
           if (live[k] && quad == 0) {
             const float lse =
-                l[k] > 0.f ? (rowfac[k] * m[k] + __log2f(l[k])) * 0.69314718055994531f : -INFINITY;
+                l[k] > 0.f
+                    ? ((kTree ? m[k] : rowfac[k] * m[k]) + __log2f(l[k])) * 0.69314718055994531f
+                    : -INFINITY;
             if (ns == 1) p.lse[qrow_off[k]] = lse;
             else lse_part[prow[k]] = lse;
           }
