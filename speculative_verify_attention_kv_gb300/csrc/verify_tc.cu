@@ -87,6 +87,7 @@ constexpr int kProducerWarp = kPvWarp + 1;
 constexpr int kThreads = 32 * (kProducerWarp + 1);
 static_assert(kThreads == 512, "warp roles");
 static_assert(kStages == 2, "one QK-issuing warp per S/P buffer");
+static_assert(kRing == kScStages, "trees free a tile's codes and scales by one barrier");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;          // lazy rescale threshold (factor 256)
 
@@ -357,6 +358,29 @@ __device__ __forceinline__ void stage_scales(const AttnParams& p, const Seg& s, 
                : "memory");
 }
 
+// The codes and scale rows of tile `it` of segment s into L2, given the id of its page
+// (lane & 3): bulk prefetches of the code blocks, plain ones of the 64-byte scale rows
+// (bulk prefetches of those measured slower).
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const AttnParams& p, const Seg& s, int it, int pg,
+                                              int lane) {
+  const int k0 = it * kTileKeys;
+  // the pages stage_codes will copy: inside the sequence and not wholly below a
+  // sliding window
+  const bool want = it < s.i1 && k0 + kPageSize * (lane & 3) < s.Lk &&
+                    k0 + kPageSize * ((lane & 3) + 1) > s.klo;
+  if (want && lane < kPagesPerTile && pg >= 0 && pg < p.num_pages)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                 ::"l"(p.k_pages + code_offset(pg, s.h, p.num_kv_heads, 0, D)),
+                 "r"((uint32_t)(2 * kPageSize * D)) : "memory");
+  const int pgs = __shfl_sync(0xffffffffu, pg, lane & 3);
+  if (want && lane >= 4 && lane < 12 && pgs >= 0 && pgs < p.num_pages) {
+    const size_t sc = ((size_t)pgs * p.num_kv_heads + s.h) * kPageSize;
+    const float* src = (lane < 8 ? p.k_scales : p.v_scales) + sc;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+  }
+}
+
 // Tile row of key n: keys are permuted inside a tile (K and V alike, so the
 // contraction over keys is unchanged) so that S/P column 8i + 2q + b, which the
 // 16x256b TMEM load hands to the thread with q = lane % 4, holds key
@@ -407,6 +431,52 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
   }
 }
 
+// The same with every address but the first a constant away: pass q's key and tile row
+// differ from pass 0's by constants, and the swizzle's row bits are free of carries, so
+// that a store's address is one exclusive or (and an offset in the instruction).
+template <int D>
+__device__ __forceinline__ void convert_codes_fast(const uint8_t* src, uint8_t* dst, int lt) {
+  constexpr int kPageStride = 2 * kPageSize * D;
+  constexpr int kChunks = D / 16;
+  constexpr int kQuartersPerPair = kChunks / 4;
+  constexpr int kKeysPerPass = kLoadThreads * 16 / D;             // 8, 16 or 32
+  constexpr int kPer = kTileKeys / kKeysPerPass;
+  const int w = lt >> 5, l = lt & 31, qtr = l >> 3, rsel = (l >> 2) & 1, j = l & 3;
+  const int pair = qtr / kQuartersPerPair, qq = qtr % kQuartersPerPair;
+  const int c16 = D == 64 ? j : 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
+  const int key0 = w * (32 * 16 / D) + 2 * pair + rsel;           // of pass 0, < kKeysPerPass
+  const uint32_t from = smem_u32(src) + (key0 / kPageSize) * kPageStride +
+                        (key0 % kPageSize) * D + c16 * 16;
+  const int n0 = tile_row_of_key(key0), c8 = 2 * c16;
+  const uint32_t to = smem_u32(dst) + (c8 / 8) * (kTileKeys * 128) + n0 * 128 +
+                      (((c8 & 7) ^ (n0 & 7)) << 4);
+  uint4 wv[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    constexpr int kHalf = kPageSize / 8;                          // 8-key passes of a page
+    const int step = kKeysPerPass == 8 ? (q / kHalf) * kPageStride + (q % kHalf) * 8 * D
+                                       : q * (kKeysPerPass / kPageSize) * kPageStride;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(wv[q].x), "=r"(wv[q].y), "=r"(wv[q].z), "=r"(wv[q].w) : "r"(from + step));
+  }
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    // tile rows of pass q are dn further on, dn's low three bits free in n0
+    const int dn = kKeysPerPass == 8 ? 32 * (q & 1) + 2 * (q >> 1)
+                                     : 2 * q * (kKeysPerPass / kPageSize);
+    uint4 h0, h1;
+    i8x4_to_h2x2(wv[q].x, h0.x, h0.y);
+    i8x4_to_h2x2(wv[q].y, h0.z, h0.w);
+    i8x4_to_h2x2(wv[q].z, h1.x, h1.y);
+    i8x4_to_h2x2(wv[q].w, h1.z, h1.w);
+    const uint32_t at = to ^ ((dn & 7) << 4);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dn * 128), "r"(h0.x),
+                 "r"(h0.y), "r"(h0.z), "r"(h0.w) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"((at ^ 16) + dn * 128),
+                 "r"(h1.x), "r"(h1.y), "r"(h1.z), "r"(h1.w) : "memory");
+  }
+}
+
 // ------------------------------------------------------------------- kernel
 // kSwa: sliding-window instantiation (window read from the parameters); the
 // plain one compiles the window bounds out. kItems: the plan holds prefix
@@ -438,7 +508,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(smem_u32(&sh->ring_full[s]), 1);
-      for (int kv = 0; kv < 2; ++kv) mbar_init(smem_u32(&sh->ring_empty[kv][s]), kLoadWarps);
+      // trees: ring_empty[0] alone, for the codes and the scales of the tile
+      for (int kv = 0; kv < 2; ++kv)
+        mbar_init(smem_u32(&sh->ring_empty[kv][s]),
+                  kTree ? 2 * kLoadWarps + kSoftmaxWarps : kLoadWarps);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh->k_full[s]), kLoadWarps);
@@ -783,7 +856,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&sh->p_full[st]));
-            mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
+            mbar_arrive(smem_u32(&sh->ring_empty[0][sst]));  // the scales are read
           }
           if (++sst == kScStages) sst = 0, sc_phase ^= 1;
         }
@@ -1035,7 +1108,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
              sync.wait(smem_u32(&sh->k_free[st]), ((g / kStages) & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        convert_codes<D>(stage, kbuf + st * C::kTileBytes, lt);
+        if constexpr (kTree) convert_codes_fast<D>(stage, kbuf + st * C::kTileBytes, lt);
+        else convert_codes<D>(stage, kbuf + st * C::kTileBytes, lt);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1045,11 +1119,14 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // V codes -> fp16 V tile
         ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->v_free[vst]), ((g / kVStages) & 1) ^ 1));
         if (!ok) break;
-        convert_codes<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
+        if constexpr (kTree)
+          convert_codes_fast<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
+        else
+          convert_codes<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sh->ring_empty[1][r]));
+          mbar_arrive(smem_u32(&sh->ring_empty[kTree ? 0 : 1][r]));
           mbar_arrive(smem_u32(&sh->v_full[vst]));
         }
       }
@@ -1069,39 +1146,20 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // g - kRing, scales once the softmax is done with those of g - kScStages
         if (lane == 0)
           ok = sync.wait(smem_u32(&sh->ring_empty[0][r]), ph) &&
-               sync.wait(smem_u32(&sh->ring_empty[1][r]), ph) &&
-               sync.wait(smem_u32(&sh->sc_free[sst]), ((g / kScStages) & 1) ^ 1);
+               (kTree || (sync.wait(smem_u32(&sh->ring_empty[1][r]), ph) &&
+                          sync.wait(smem_u32(&sh->sc_free[sst]), ((g / kScStages) & 1) ^ 1)));
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         const int page = stage_codes<D>(p, s, it, stage, smem_u32(&sh->ring_full[r]), lane, win);
         stage_scales(p, s, page, scales + sst * 2 * kTileKeys, smem_u32(&sh->sc_full[sst]), lane);
         ++armed;
-        {
-          // the codes of the tile kRing ahead into L2 only (no shared
-          // memory): its staging copy, issued when this ring stage frees
-          // again, then hits L2. Measured 5-6% faster on 16 x 32K and the
-          // ragged batch; 2 to 4 tiles ahead do the same, 6 less. The scale
-          // rows take plain L2 prefetches (bulk prefetches of 64 bytes each
-          // measured slower).
-          const int ahead = it + kRing;
-          const int k0a = ahead * kTileKeys;
-          const int pg = win.peek(s.b, k0a / kPageSize + (lane & 3));
-          // the pages stage_codes will copy: inside the sequence and not
-          // wholly below a sliding window
-          const bool want = ahead < s.i1 && k0a + kPageSize * (lane & 3) < s.Lk &&
-                            k0a + kPageSize * ((lane & 3) + 1) > s.klo;
-          if (want && lane < kPagesPerTile && pg >= 0 && pg < p.num_pages)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
-                         ::"l"(p.k_pages + code_offset(pg, s.h, p.num_kv_heads, 0, D)),
-                         "r"((uint32_t)(2 * kPageSize * D)) : "memory");
-          // and its K / V scale rows (64 bytes each) with plain L2 prefetches
-          const int pgs = __shfl_sync(0xffffffffu, pg, lane & 3);
-          if (want && lane >= 4 && lane < 12 && pgs >= 0 && pgs < p.num_pages) {
-            const size_t sc = ((size_t)pgs * p.num_kv_heads + s.h) * kPageSize;
-            const float* src = (lane < 8 ? p.k_scales : p.v_scales) + sc;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
-          }
-        }
+        // The codes of the tile kRing ahead into L2 only (no shared memory): its
+        // staging copy, issued when this ring stage frees again, then hits L2.
+        // Measured 5-6% faster on 16 x 32K and the ragged batch; 2 to 4 tiles
+        // ahead do the same, 6 less. (For trees, on the PV issuer's warp instead: 274
+        // -> 292 to 325 us.)
+        const int ahead = it + kRing;
+        prefetch_tile<D>(p, s, ahead, win.peek(s.b, ahead * kPagesPerTile + (lane & 3)), lane);
       }
     }
     // copies still in flight (only after an abort: on the normal path the
