@@ -723,28 +723,30 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         float limit[2] = {-INFINITY, -INFINITY};
         for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
           const int st = g % kStages;
-          ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1));
-          if (!ok) break;                                   // a timeout seen by some lanes
-          fence_after();
-          if (warp_live) {
-            uint32_t pw[16];                                // P: 32 packed columns
-            uint32_t sv[32];
-            tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
-            // the scales' barrier and the K scales while the TMEM load is in flight
-            ok = sync.wait(smem_u32(&sh->sc_full[sst]), sc_phase);
-            const int k0 = it * kTileKeys;
-            const float* ks = scales + sst * 2 * kTileKeys;
-            const float* vs = ks + kTileKeys;
-            float2 ks2[8], x[2][8];
+          // what need not follow S comes before the wait for it: the tile's scales
+          const float* ks = scales + sst * 2 * kTileKeys;
+          const float* vs = ks + kTileKeys;
+          float2 ks2[8];
+          ok = sync.wait(smem_u32(&sh->sc_full[sst]), sc_phase);
+          if (warp_live && ok) {
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
               const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
               ks2[2 * i4] = make_float2(kq.x, kq.y);
               ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
             }
+          }
+          ok = ok && sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;                                   // a timeout seen by some lanes
+          fence_after();
+          if (warp_live) {
+            uint32_t pw[16];                                // P: 32 packed columns
+            uint32_t sv[32];
+            tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
+            const int k0 = it * kTileKeys;
+            float2 x[2][8];
             tmem_wait_ld(sv);         // sv is read only after the wait
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -1203,8 +1205,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           const int st = g % kStages, vst = g % kVStages;
           if (is_qk) {
             if (st != qk_par) continue;
-            ok = sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1) &&
-                 sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1);
+            // (trees: the tile is converted before the buffer is free)
+            ok = (!kTree || sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1)) &&
+                 sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1) &&
+                 (kTree || sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1));
             if (!ok) break;
             fence_after();
 #pragma unroll
@@ -1216,8 +1220,9 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             mma_commit(smem_u32(&sh->s_full[st]));
             mma_commit(smem_u32(&sh->k_free[st]));
           } else {
-            ok = sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1) &&
-                 sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1);
+            ok = (!kTree || sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1)) &&
+                 sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1) &&
+                 (kTree || sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1));
             if (!ok) break;
             fence_after();
 #pragma unroll
