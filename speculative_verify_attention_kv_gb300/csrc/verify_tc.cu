@@ -72,10 +72,6 @@ using namespace dev;
 
 constexpr int kTileKeys = 64;
 constexpr int kPagesPerTile = kTileKeys / kPageSize;
-constexpr int kStages = 2;                    // S/P buffers in TMEM, fp16 K tiles
-constexpr int kVStages = 2;                   // fp16 V tiles
-constexpr int kScStages = 3;                  // K/V scale arrays
-constexpr int kRing = 3;                      // int8 staging stages
 constexpr int kSoftmaxWarps = 8;              // 2 per TMEM lane quarter, 16 rows each
 constexpr int kLoadWarps = 4;
 constexpr int kLoadThreads = 32 * kLoadWarps;
@@ -86,17 +82,25 @@ constexpr int kProducerWarp = kPvWarp + 1;
 // 16 warps = 4 per SM sub-partition, so each thread may hold 128 registers
 constexpr int kThreads = 32 * (kProducerWarp + 1);
 static_assert(kThreads == 512, "warp roles");
-static_assert(kStages == 2, "one QK-issuing warp per S/P buffer");
-static_assert(kRing == kScStages, "trees free a tile's codes and scales by one barrier");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;          // lazy rescale threshold (factor 256)
 
-template <int D>
+// Trees with heads of 64 or 128 have room for more of everything, which takes the wait
+// for a buffer out of the chain QK -> softmax -> PV -> QK, and for a ring so deep that
+// no prefetch has to run ahead of it.
+template <int D, bool kTree>
 struct Cfg {
+  static constexpr bool kDeep = kTree && D <= 128;
+  static constexpr int kStages = kDeep ? 4 : 2;       // S/P buffers in TMEM, fp16 K tiles
+  static constexpr int kVStages = kDeep ? 4 : 2;      // fp16 V tiles
+  static constexpr int kRing = !kDeep ? 3 : D == 128 ? 5 : 8;     // int8 staging stages
+  static constexpr int kScStages = kRing;             // K/V scale arrays
+  static constexpr bool kPrefetch = !kDeep;           // the tile a ring ahead into L2
+  static_assert(kStages % 2 == 0, "QK-issuing warps by parity");
   static constexpr int kTileBytes = kTileKeys * D * 2;          // fp16 tile
   static constexpr int kQCol = 0;                                // Q': D/2 columns
   static constexpr int kSCol = D / 2;                            // S[2]: 64 columns each
-  static constexpr int kOCol = D / 2 + 2 * kTileKeys;            // O: D columns
+  static constexpr int kOCol = D / 2 + kStages * kTileKeys;      // O: D columns
   static_assert(kOCol + D <= (int)kTmemCols, "TMEM budget");
   // staging ring stage: 4 (page, KV head) blocks of [K codes 16 x D][V codes 16 x D]
   static constexpr int kRingStage = 2 * kTileKeys * D;
@@ -106,7 +110,7 @@ struct Cfg {
   static constexpr int kOffRing = kOffV + kVStages * kTileBytes;         // int8 [kRing]
   static constexpr int kOffScales = kOffRing + kRing * kRingStage;       // fp32 [kScStages][2][64]
   static constexpr int kOffBars = kOffScales + kScStages * 2 * kTileKeys * 4;
-  static constexpr int kBarBytes = 512;
+  static constexpr int kBarBytes = kDeep ? 1024 : 512;
   static constexpr int kSmemUsed = kOffBars + kBarBytes;
   // + up to 1 KB to align the base (the kernel checks the room it got); at
   // least 120 KB so that one CTA (and its 512 TMEM columns) owns the SM
@@ -245,7 +249,10 @@ make_iter(const int* stp, const int* seq_T, const int* seq_ctx, const ItemDesc* 
     return SegIter{stp, seq_T, seq_ctx, B, G, Hkv, window, t, t_end};
 }
 
+template <class C>
 struct Smem {
+  static constexpr int kRing = C::kRing, kScStages = C::kScStages, kStages = C::kStages,
+                       kVStages = C::kVStages;
   uint64_t ring_full[kRing];      // producer tx (K and V codes) -> converters
   uint64_t ring_empty[2][kRing];  // converters done with a stage's [0] K / [1] V codes -> producer
   uint64_t sc_full[kScStages];    // producer cp.async (scales) -> softmax
@@ -486,7 +493,10 @@ template <int D, bool kSwa, bool kItems, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::type p) {
   static_assert(kSwa + kItems + kTree <= 1, "prefix groups and trees are planned without a window");
-  using C = Cfg<D>;
+  using C = Cfg<D, kTree>;
+  using Smem = tc::Smem<C>;
+  constexpr int kStages = C::kStages, kVStages = C::kVStages, kScStages = C::kScStages,
+                kRing = C::kRing;
   static_assert(sizeof(Smem) <= C::kBarBytes, "barrier area");
   extern __shared__ uint8_t smem_raw[];
   allow_dependent_launch();
@@ -1160,8 +1170,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // Measured 5-6% faster on 16 x 32K and the ragged batch; 2 to 4 tiles
         // ahead do the same, 6 less. (For trees, on the PV issuer's warp instead: 274
         // -> 292 to 325 us.)
-        const int ahead = it + kRing;
-        prefetch_tile<D>(p, s, ahead, win.peek(s.b, ahead * kPagesPerTile + (lane & 3)), lane);
+        if constexpr (C::kPrefetch) {
+          const int ahead = it + kRing;
+          prefetch_tile<D>(p, s, ahead, win.peek(s.b, ahead * kPagesPerTile + (lane & 3)), lane);
+        }
       }
     }
     // copies still in flight (only after an abort: on the normal path the
@@ -1182,6 +1194,70 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     // i - 2) has completed (issue order alone does not order a later TMEM
     // write after an earlier MMA's read).
     // warp kPvWarp: PV(i) into O once the softmax has written P(i).
+    if constexpr (kTree) {
+      // the warp as one, so that addresses and descriptors can stay uniform; one lane
+      // issues
+      constexpr uint32_t kIdescQK = idesc_f16(128, kTileKeys, 0, 0);
+      constexpr uint32_t kIdescPV = idesc_f16(128, D, 0, 1);
+      const uint64_t kdesc0 = sdesc(smem_u32(kbuf), 16, 1024);
+      const uint64_t vdesc0 = sdesc(smem_u32(vbuf), kTileKeys * 128, 1024);
+      const bool leader = elect_one();
+      const int role = warp - kMmaWarp;             // 0, 1: QK of even, odd tiles; 2: PV
+      int g = 0, nsegs = 0;
+      Seg s;
+      bool ok = true;
+      while (ok && iter.next(s)) {
+        if (role < 2) {
+          ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->q_full), nsegs & 1));
+          if (!ok) break;
+          fence_after();
+          if (leader) mbar_arrive(smem_u32(&sh->q_ack));
+        }
+        for (int it = s.i0; it < s.i1; ++it, ++g) {
+          const int st = g % kStages;
+          if (role < 2) {
+            if (st % 2 != role) continue;
+            ok = sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1) &&
+                 sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + C::kSCol + st * kTileKeys, tmem + C::kQCol + kk * 8,
+                       kdesc0 + (uint64_t)((st * C::kTileBytes + (kk / 4) * (kTileKeys * 128) +
+                                            (kk % 4) * 32) >> 4),
+                       kIdescQK, kk > 0);
+              mma_commit(smem_u32(&sh->s_full[st]));
+              mma_commit(smem_u32(&sh->k_free[st]));
+            }
+          } else {
+            ok = sync.wait(smem_u32(&sh->v_full[st]), (g / kStages) & 1) &&
+                 sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                mma_ts(tmem + C::kOCol, tmem + C::kSCol + st * kTileKeys + kk * 8,
+                       vdesc0 + (uint64_t)((st * C::kTileBytes + kk * 16 * 128) >> 4), kIdescPV,
+                       (it == s.i0 && kk == 0) ? 0u : 1u);
+              mma_commit(smem_u32(&sh->v_free[st]));
+              mma_commit(smem_u32(&sh->p_free[st]));
+            }
+          }
+          __syncwarp();
+        }
+        ++nsegs;
+      }
+      if (leader) {                                 // as below
+        mma_commit(smem_u32(&sh->drain[role]));
+        sync.drain(smem_u32(&sh->drain[role]), 0);
+      }
+      __syncwarp();
+    } else {
     const bool is_qk = warp != kPvWarp;
     const int qk_par = warp - kMmaWarp;          // tiles of this parity (QK issuers)
     const int role = is_qk ? qk_par : 2;
@@ -1204,7 +1280,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
           const int st = g % kStages, vst = g % kVStages;
           if (is_qk) {
-            if (st != qk_par) continue;
+            if (st % 2 != qk_par) continue;
             // (trees: the tile is converted before the buffer is free)
             ok = (!kTree || sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1)) &&
                  sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1) &&
@@ -1242,6 +1318,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       mma_commit(smem_u32(&sh->drain[role]));
       sync.drain(smem_u32(&sh->drain[role]), 0);
     }
+    }
     __syncwarp();
   }
 
@@ -1263,7 +1340,7 @@ cudaError_t launch_verify_tc(const AttnParams& p, int rows_cap, int ncta, bool i
   (void)rows_cap;
 #define SPLASH_TC(DD, SWA, IT)                                                                 \
   do {                                                                                         \
-    constexpr int smem = tc::Cfg<DD>::kSmemBytes;                                              \
+    constexpr int smem = tc::Cfg<DD, false>::kSmemBytes;                                       \
     cudaError_t e = ensure_dynamic_smem<tc::verify_tc_kernel<DD, SWA, IT, false>>(smem);      \
     if (e != cudaSuccess) return e;                                                            \
     e = launch_dependent(tc::verify_tc_kernel<DD, SWA, IT, false>, dim3(ncta),                 \
@@ -1294,11 +1371,12 @@ cudaError_t launch_verify_tree(const TreeAttnParams& p, int ncta, bool planned,
                                cudaStream_t stream) {
 #define SPLASH_TREE(DD)                                                                        \
   do {                                                                                         \
-    constexpr int smem = tc::Cfg<DD>::kSmemBytes;                                              \
+    using C = tc::Cfg<DD, true>;                                                               \
+    constexpr int smem = C::kSmemBytes;                                                        \
     constexpr auto kernel = tc::verify_tc_kernel<DD, false, false, true>;                      \
     cudaError_t e = ensure_dynamic_smem<kernel>(smem);                                         \
     if (e != cudaSuccess) return e;                                                            \
-    static_assert(kTreePlanRoom <= 2 * tc::Cfg<DD>::kTileBytes * tc::kStages, "plan's room");  \
+    static_assert(kTreePlanRoom <= C::kOffRing, "plan's room");                                \
     if (planned)                                                                               \
       return launch_dependent(kernel, dim3(ncta), dim3(tc::kThreads), smem, stream, p);        \
     kernel<<<ncta, tc::kThreads, smem, stream>>>(p);                                           \
