@@ -438,49 +438,54 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
   }
 }
 
-// The same with every address but the first a constant away: pass q's key and tile row
-// differ from pass 0's by constants, and the swizzle's row bits are free of carries, so
-// that a store's address is one exclusive or (and an offset in the instruction).
-template <int D>
+// The same by kWarps warps, with every address but the first a constant away: pass q's
+// key and tile row differ from pass 0's by constants, and the swizzle's row bits are free
+// of carries, so that a store's address is one exclusive or (and an offset in the
+// instruction).
+template <int D, int kWarps>
 __device__ __forceinline__ void convert_codes_fast(const uint8_t* src, uint8_t* dst, int lt) {
   constexpr int kPageStride = 2 * kPageSize * D;
-  constexpr int kChunks = D / 16;
-  constexpr int kQuartersPerPair = kChunks / 4;
-  constexpr int kKeysPerPass = kLoadThreads * 16 / D;             // 8, 16 or 32
+  constexpr int kQuartersPerPair = D / 64;
+  constexpr int kKeysPerPass = kWarps * 512 / D;                  // 4, 8, 16 or 32
   constexpr int kPer = kTileKeys / kKeysPerPass;
+  constexpr int kPerPage = kKeysPerPass < kPageSize ? kPageSize / kKeysPerPass : 1;
+  constexpr int kPages = kKeysPerPass < kPageSize ? 1 : kKeysPerPass / kPageSize;
+  constexpr int kBatch = kPer < 8 ? kPer : 8;                     // loads in flight
   const int w = lt >> 5, l = lt & 31, qtr = l >> 3, rsel = (l >> 2) & 1, j = l & 3;
   const int pair = qtr / kQuartersPerPair, qq = qtr % kQuartersPerPair;
   const int c16 = D == 64 ? j : 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
-  const int key0 = w * (32 * 16 / D) + 2 * pair + rsel;           // of pass 0, < kKeysPerPass
+  const int key0 = w * (512 / D) + 2 * pair + rsel;               // of pass 0, < kKeysPerPass
   const uint32_t from = smem_u32(src) + (key0 / kPageSize) * kPageStride +
                         (key0 % kPageSize) * D + c16 * 16;
   const int n0 = tile_row_of_key(key0), c8 = 2 * c16;
   const uint32_t to = smem_u32(dst) + (c8 / 8) * (kTileKeys * 128) + n0 * 128 +
                       (((c8 & 7) ^ (n0 & 7)) << 4);
-  uint4 wv[kPer];
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    constexpr int kHalf = kPageSize / 8;                          // 8-key passes of a page
-    const int step = kKeysPerPass == 8 ? (q / kHalf) * kPageStride + (q % kHalf) * 8 * D
-                                       : q * (kKeysPerPass / kPageSize) * kPageStride;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(wv[q].x), "=r"(wv[q].y), "=r"(wv[q].z), "=r"(wv[q].w) : "r"(from + step));
-  }
+  for (int q0 = 0; q0 < kPer; q0 += kBatch) {
+    uint4 wv[kBatch];
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    // tile rows of pass q are dn further on, dn's low three bits free in n0
-    const int dn = kKeysPerPass == 8 ? 32 * (q & 1) + 2 * (q >> 1)
-                                     : 2 * q * (kKeysPerPass / kPageSize);
-    uint4 h0, h1;
-    i8x4_to_h2x2(wv[q].x, h0.x, h0.y);
-    i8x4_to_h2x2(wv[q].y, h0.z, h0.w);
-    i8x4_to_h2x2(wv[q].z, h1.x, h1.y);
-    i8x4_to_h2x2(wv[q].w, h1.z, h1.w);
-    const uint32_t at = to ^ ((dn & 7) << 4);
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dn * 128), "r"(h0.x),
-                 "r"(h0.y), "r"(h0.z), "r"(h0.w) : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"((at ^ 16) + dn * 128),
-                 "r"(h1.x), "r"(h1.y), "r"(h1.z), "r"(h1.w) : "memory");
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u;
+      const int step = q / kPerPage * kPages * kPageStride + q % kPerPage * kKeysPerPass * D;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(wv[u].x), "=r"(wv[u].y), "=r"(wv[u].z), "=r"(wv[u].w) : "r"(from + step));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u;
+      // tile rows of pass q are dn further on, dn's low three bits free in n0
+      const int dn = 2 * (q / kPerPage) * kPages + q % kPerPage * kKeysPerPass * 4;
+      uint4 h0, h1;
+      i8x4_to_h2x2(wv[u].x, h0.x, h0.y);
+      i8x4_to_h2x2(wv[u].y, h0.z, h0.w);
+      i8x4_to_h2x2(wv[u].z, h1.x, h1.y);
+      i8x4_to_h2x2(wv[u].w, h1.z, h1.w);
+      const uint32_t at = to ^ ((dn & 7) << 4);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dn * 128), "r"(h0.x),
+                   "r"(h0.y), "r"(h0.z), "r"(h0.w) : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"((at ^ 16) + dn * 128),
+                   "r"(h1.x), "r"(h1.y), "r"(h1.z), "r"(h1.w) : "memory");
+    }
   }
 }
 
@@ -497,6 +502,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   using Smem = tc::Smem<C>;
   constexpr int kStages = C::kStages, kVStages = C::kVStages, kScStages = C::kScStages,
                 kRing = C::kRing;
+  // converter warps of a K or V tile: for trees two each, side by side
+  constexpr int kConvertWarps = kTree ? kLoadWarps / 2 : kLoadWarps;
   static_assert(sizeof(Smem) <= C::kBarBytes, "barrier area");
   extern __shared__ uint8_t smem_raw[];
   allow_dependent_launch();
@@ -521,10 +528,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       // trees: ring_empty[0] alone, for the codes and the scales of the tile
       for (int kv = 0; kv < 2; ++kv)
         mbar_init(smem_u32(&sh->ring_empty[kv][s]),
-                  kTree ? 2 * kLoadWarps + kSoftmaxWarps : kLoadWarps);
+                  kTree ? kLoadWarps + kSoftmaxWarps : kLoadWarps);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sh->k_full[s]), kLoadWarps);
+      mbar_init(smem_u32(&sh->k_full[s]), kConvertWarps);
       mbar_init(smem_u32(&sh->k_free[s]), 1);
       mbar_init(smem_u32(&sh->s_full[s]), 1);
       mbar_init(smem_u32(&sh->p_full[s]), kSoftmaxWarps);
@@ -536,7 +543,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(smem_u32(&sh->v_free[s]), 1);
-      mbar_init(smem_u32(&sh->v_full[s]), kLoadWarps);
+      mbar_init(smem_u32(&sh->v_full[s]), kConvertWarps);
     }
     mbar_init(smem_u32(&sh->q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&sh->q_ack), 2);
@@ -630,7 +637,11 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       size_t qrow_off[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int i = ln[k] & 31, r = (ln[k] >> 5) * rpq + i;
+        // (trees: a quarter's rows go in eights to its two warps in turn, so that up to
+        // 64 rows give every softmax warp one set of them instead of four warps two)
+        const int li = ln[k] & 31;
+        const int i = kTree ? (li >> 3 & 1) * 16 + (li >> 4) * 8 + (li & 7) : li;
+        const int r = (ln[k] >> 5) * rpq + i;
         live[k] = i < rpq && r < s.R;
         rr[k] = live[k] ? r : -1;
         if constexpr (kItems || kTree) {
@@ -1106,6 +1117,37 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     }
   } else if (warp < kSoftmaxWarps + kLoadWarps) {
     // =========================================================== converters
+    if constexpr (kTree) {
+      // two warps for the K codes of every tile and two for the V codes: a wait costs a
+      // warp 150 cycles and more even where there is nothing to wait for, and this way
+      // the ones' waits run beside the others' work
+      const int half = warp - kSoftmaxWarps >= kConvertWarps ? 1 : 0;
+      const int lt = tid - 32 * (kSoftmaxWarps + half * kConvertWarps);
+      uint8_t* to = half ? vbuf : kbuf;
+      uint64_t* free = half ? sh->v_free : sh->k_free;
+      uint64_t* ready = half ? sh->v_full : sh->k_full;
+      static_assert(kStages == kVStages, "K and V tiles alike");
+      int g = 0;
+      Seg s;
+      bool ok = true;
+      while (ok && iter.next(s)) {
+        for (int it = s.i0; it < s.i1; ++it, ++g) {
+          const int r = g % kRing, st = g % kStages;
+          ok = sync.wait(smem_u32(&sh->ring_full[r]), (g / kRing) & 1) &&
+               sync.wait(smem_u32(&free[st]), ((g / kStages) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          convert_codes_fast<D, kConvertWarps>(ring + r * C::kRingStage + half * kPageSize * D,
+                                               to + st * C::kTileBytes, lt);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sh->ring_empty[0][r]));
+            mbar_arrive(smem_u32(&ready[st]));
+          }
+        }
+      }
+    } else {
     const int lt = tid - 32 * kSoftmaxWarps;
     int g = 0;
     Seg s;
@@ -1120,8 +1162,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
              sync.wait(smem_u32(&sh->k_free[st]), ((g / kStages) & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if constexpr (kTree) convert_codes_fast<D>(stage, kbuf + st * C::kTileBytes, lt);
-        else convert_codes<D>(stage, kbuf + st * C::kTileBytes, lt);
+        convert_codes<D>(stage, kbuf + st * C::kTileBytes, lt);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1131,17 +1172,15 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // V codes -> fp16 V tile
         ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->v_free[vst]), ((g / kVStages) & 1) ^ 1));
         if (!ok) break;
-        if constexpr (kTree)
-          convert_codes_fast<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
-        else
-          convert_codes<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
+        convert_codes<D>(stage + kPageSize * D, vbuf + vst * C::kTileBytes, lt);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sh->ring_empty[kTree ? 0 : 1][r]));
+          mbar_arrive(smem_u32(&sh->ring_empty[1][r]));
           mbar_arrive(smem_u32(&sh->v_full[vst]));
         }
       }
+    }
     }
   } else if (warp >= kProducerWarp) {
     // ============================================================ producer
