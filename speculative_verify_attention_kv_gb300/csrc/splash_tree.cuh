@@ -27,6 +27,13 @@ __host__ __device__ inline RowBlocks row_blocks(int T, int group) {
 // KV head, row block), the blocks of a head next to each other; the rows of a sequence
 // lie at the sum of the caller's lengths before it, a rejected sequence's too.
 constexpr int kTreeTile = 64;
+// What a segment costs beside its tiles, in the units of tile_cost. A tile of a tree's
+// kernel takes less time than one of a plain block's, so the fill and the last rows'
+// way out weigh more of them: us at 6 / 9 / 13 / 20 tiles, 32 sequences of 1024..32768
+// keys 172 / 156 / 157 / 170; 20 of 300..12000 keys 43.1 / 41.1 / 43.1 / 45.6; 30 of
+// 100..30000 keys, heads of 64, 109 / 111 / 115 / 121; 12 of 1000..9000 keys, heads of
+// 256, 76.1 / 72.6 / 76.0 / 79.6; 16 equal sequences 264 / 264 / 265 / 269.
+constexpr long long kTreeSegmentCost = 9 * 4096;
 struct TreeSeq {
   bool ok;               // lengths in range; else T = ctx = 0
   int T, ctx;
@@ -45,7 +52,7 @@ struct TreeSeq {
   __device__ long long units(int hkv) const { return (long long)hkv * rb.count; }
   __device__ long long unit_cost() const {
     return (long long)tiles * (tile_cost(kClassTensor) + row_cost(kClassTensor) * rb.rows) +
-           segment_cost(kClassTensor);
+           kTreeSegmentCost;
   }
 };
 
@@ -79,7 +86,9 @@ struct TreeLayout {
 };
 
 // Batches that the attention kernel plans by itself, every CTA alike, with a thread
-// per sequence: a plan costs it about a microsecond, a launch before it three.
+// per sequence. It costs about what a launch before it would (5500 clocks, 3 us, at 16
+// sequences), but the pipeline's set-up and the tensor maps' fetch run beside it: a call
+// of one sequence 16.5 us, with the planner as a launch 18.5.
 constexpr int kTreeSelfPlan = 512;
 
 __host__ __device__ inline TreeLayout make_tree_layout(int B, int D, long long rows_bound) {
@@ -175,7 +184,7 @@ __device__ inline int plan_tree(const TreeAttnParams& p, const PlanArrays& a, in
   const int n = min(min(ncta, total), kMaxCtas);
   if (tid == 0) *a.carry = INT_MIN;
   // CTA k starts where the cumulative cost reaches k / n of the total: the
-  // sequence, then the unit, then the tile (a unit's first segment_cost maps to
+  // sequence, then the unit, then the tile (a unit's first kTreeSegmentCost maps to
   // its first tile); then the starts are made strictly increasing, the last
   // ones pulled back so that every CTA has a tile
   for (int base = 0; n > 0 && base <= n; base += threads) {
@@ -190,7 +199,7 @@ __device__ inline int plan_tree(const TreeAttnParams& p, const PlanArrays& a, in
                       p.max_pages_per_seq);
       const long long uc = s.unit_cost(), off = target - a.cost[b];
       const int u = (int)min(off / uc, s.units(hkv) - 1);
-      const long long rem = off - u * uc - segment_cost(kClassTensor);
+      const long long rem = off - u * uc - kTreeSegmentCost;
       const long long w = tile_cost(kClassTensor) + row_cost(kClassTensor) * s.rb.rows;
       const int t = rem < 0 ? 0 : (int)min(rem / w, (long long)s.tiles - 1);
       start = a.stp[b] + u * s.tiles + t;
