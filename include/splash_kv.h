@@ -636,7 +636,8 @@ int splash_choose_targets(const void* logits, int dtype, long long logits_stride
  *
  * splash_choose_targets counts a block's own tokens x_0 .. x_t for row t, which is
  * a chain's history: for a tree leave its penalties out, or keep them to committed
- * tokens by passing block_tokens of -1.
+ * tokens by passing block_tokens of -1. It takes at most 128 rows a sequence: the rows
+ * of a larger tree go to it as several sequences.
  * ------------------------------------------------------------------------ */
 
 /*

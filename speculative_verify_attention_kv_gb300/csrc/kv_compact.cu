@@ -58,12 +58,13 @@ __global__ void __launch_bounds__(kThreads, 8) kv_compact_kernel(CompactParams p
     from = p.path_rows[first + 1 + lane];
     dst = p.slots[first + 1 + lane];
   }
-  const int count = p.accepted[b] + 1;
-  if (count <= 1) return;                        // the root is where it belongs
-  if (!usable || count > end - first) {
+  const int accepted = p.accepted[b];
+  if (accepted <= 0) return;                     // the root is where it belongs
+  if (!usable || accepted >= end - first) {
     if (lane == 0) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
     return;
   }
+  const int count = accepted + 1;
   for (int base = 1; base < count; base += 32) {
     const int i = base + lane;
     if (base > 1 && i < count) {

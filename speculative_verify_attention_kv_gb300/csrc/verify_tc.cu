@@ -512,6 +512,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
                                              ~uintptr_t(1023));
   if (smem - smem_raw + C::kSmemUsed > C::kSmemBytes) {
     if (threadIdx.x == 0) report(p.device_status, SPLASH_DEVICE_INTERNAL);
+    if constexpr (kTree) {                                 // nothing for the combine either
+      grid_dependency_wait();
+      if (blockIdx.x + threadIdx.x == 0) reinterpret_cast<TreeHeader*>(p.ws)->num_splits = 0;
+    }
     return;
   }
   uint8_t* kbuf = smem + C::kOffK;
@@ -692,6 +696,9 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           e = max(-126, min(127, e));
           up[k] = __uint_as_float((uint32_t)(e + 127) << 23);
           rowfac[k] = p.sm_scale_log2 / up[k];
+          // (trees: never 0, or a masked key's -inf would come out as NaN; such a row's
+          // scores are 0 either way)
+          if constexpr (kTree) rowfac[k] = fmaxf(rowfac[k], 1.17549435e-38f);
         }
         static_assert(D == 64 || (D / 2) % 64 == 0, "Q' stores of 64 packed columns, or 32");
         if constexpr (D == 64) {
@@ -1320,10 +1327,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           const int st = g % kStages, vst = g % kVStages;
           if (is_qk) {
             if (st % 2 != qk_par) continue;
-            // (trees: the tile is converted before the buffer is free)
-            ok = (!kTree || sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1)) &&
-                 sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1) &&
-                 (kTree || sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1));
+            ok = sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1) &&
+                 sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1);
             if (!ok) break;
             fence_after();
 #pragma unroll
@@ -1335,9 +1340,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             mma_commit(smem_u32(&sh->s_full[st]));
             mma_commit(smem_u32(&sh->k_free[st]));
           } else {
-            ok = (!kTree || sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1)) &&
-                 sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1) &&
-                 (kTree || sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1));
+            ok = sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1) &&
+                 sync.wait(smem_u32(&sh->v_full[vst]), (g / kVStages) & 1);
             if (!ok) break;
             fence_after();
 #pragma unroll
