@@ -12,7 +12,7 @@ constexpr int kMaxTreeNodes = 256;
 
 // The T * G query rows of a sequence and KV head (row t * G + g) are cut into as
 // few row blocks of at most kMaxRows as hold them, all of about the same height,
-// since a tile costs nearly the same whatever the rows (see tile_cost).
+// since a tile costs nearly the same whatever the rows (see kTreeTileCost).
 struct RowBlocks {
   int count;         // blocks
   int rows;          // rows of a block (the last may have fewer)
@@ -27,13 +27,16 @@ __host__ __device__ inline RowBlocks row_blocks(int T, int group) {
 // KV head, row block), the blocks of a head next to each other; the rows of a sequence
 // lie at the sum of the caller's lengths before it, a rejected sequence's too.
 constexpr int kTreeTile = 64;
-// What a segment costs beside its tiles, in the units of tile_cost. A tile of a tree's
-// kernel takes less time than one of a plain block's, so the fill and the last rows'
-// way out weigh more of them: us at 6 / 9 / 13 / 20 tiles, 32 sequences of 1024..32768
-// keys 172 / 156 / 157 / 170; 20 of 300..12000 keys 43.1 / 41.1 / 43.1 / 45.6; 30 of
-// 100..30000 keys, heads of 64, 109 / 111 / 115 / 121; 12 of 1000..9000 keys, heads of
-// 256, 76.1 / 72.6 / 76.0 / 79.6; 16 equal sequences 264 / 264 / 265 / 269.
-constexpr long long kTreeSegmentCost = 9 * 4096;
+// What a query row adds to a tile and a segment to its tiles, a tile being 4096. Fits of
+// the CTAs' times on ragged batches say, us a tile / row and tile / segment: heads of 256
+// 0.93 / 0.0017 / 8.2, of 128 0.63 / 0.0030 / 5.6, of 64 0.57 / 0.0021 / 3.4. Calls, mean
+// us of six ragged batches each at (row, segments in tiles) (6, 6), (6, 9), (14, 6), (14,
+// 9), (19, 9): heads of 256 71.7, 70.7, 73.0, 70.8, 71.9; of 128 55.5, 54.7, 56.5, 54.1,
+// 54.9; of 64 47.6, 48.9, 47.6, 48.6, 48.9. 32 sequences of 1024..32768 keys, heads of
+// 256: 172 us at (6, 6), 156 at (6, 9), 170 at (6, 20).
+constexpr int kTreeTileCost = 4096;
+__host__ __device__ constexpr int tree_row_cost(int D) { return D > 128 ? 6 : 14; }
+__host__ __device__ constexpr int tree_segment_cost(int D) { return (D > 64 ? 9 : 6) * 4096; }
 struct TreeSeq {
   bool ok;               // lengths in range; else T = ctx = 0
   int T, ctx;
@@ -50,9 +53,8 @@ struct TreeSeq {
     tiles = T > 0 ? (ctx + T + kTreeTile - 1) / kTreeTile : 0;
   }
   __device__ long long units(int hkv) const { return (long long)hkv * rb.count; }
-  __device__ long long unit_cost() const {
-    return (long long)tiles * (tile_cost(kClassTensor) + row_cost(kClassTensor) * rb.rows) +
-           kTreeSegmentCost;
+  __device__ long long unit_cost(int row_cost, int segment_cost) const {
+    return (long long)tiles * (kTreeTileCost + row_cost * rb.rows) + segment_cost;
   }
 };
 
@@ -114,6 +116,7 @@ struct TreeAttnParams : AttnParams {
   int num_q_tokens;
   const int32_t* tree_masks;      // [num_q_tokens, mask_stride]
   int mask_stride;
+  int row_cost, segment_cost;
 };
 
 // ------------------------------------------------------------------------- plan
@@ -154,7 +157,7 @@ __device__ inline int plan_tree(const TreeAttnParams& p, const PlanArrays& a, in
                       p.max_pages_per_seq);
       if (speaks && !s.ok) report(p.device_status, SPLASH_DEVICE_BAD_LENGTH);
       const long long units = s.T > 0 ? s.units(hkv) : 0;
-      mine = PlanSums{s.laid, units * s.tiles, units > 0 ? units * s.unit_cost() : 0};
+      mine = PlanSums{s.laid, units * s.tiles, units > 0 ? units * s.unit_cost(p.row_cost, p.segment_cost) : 0};
     }
     PlanSums incl = mine;
 #pragma unroll
@@ -184,7 +187,7 @@ __device__ inline int plan_tree(const TreeAttnParams& p, const PlanArrays& a, in
   const int n = min(min(ncta, total), kMaxCtas);
   if (tid == 0) *a.carry = INT_MIN;
   // CTA k starts where the cumulative cost reaches k / n of the total: the
-  // sequence, then the unit, then the tile (a unit's first kTreeSegmentCost maps to
+  // sequence, then the unit, then the tile (a unit's first segment cost maps to
   // its first tile); then the starts are made strictly increasing, the last
   // ones pulled back so that every CTA has a tile
   for (int base = 0; n > 0 && base <= n; base += threads) {
@@ -197,10 +200,10 @@ __device__ inline int plan_tree(const TreeAttnParams& p, const PlanArrays& a, in
       const int b = upper_index(a.cost, B - 1, target);
       const TreeSeq s(p.block_lens[b], p.context_lens[b], p.group, p.max_block_len,
                       p.max_pages_per_seq);
-      const long long uc = s.unit_cost(), off = target - a.cost[b];
+      const long long uc = s.unit_cost(p.row_cost, p.segment_cost), off = target - a.cost[b];
       const int u = (int)min(off / uc, s.units(hkv) - 1);
-      const long long rem = off - u * uc - kTreeSegmentCost;
-      const long long w = tile_cost(kClassTensor) + row_cost(kClassTensor) * s.rb.rows;
+      const long long rem = off - u * uc - p.segment_cost;
+      const long long w = kTreeTileCost + p.row_cost * s.rb.rows;
       const int t = rem < 0 ? 0 : (int)min(rem / w, (long long)s.tiles - 1);
       start = a.stp[b] + u * s.tiles + t;
     }

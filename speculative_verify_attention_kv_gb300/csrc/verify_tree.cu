@@ -267,6 +267,8 @@ int splash_verify_attention_tree(
   p.block_lens = block_lens;
   p.max_block_len = max_block_len;
   p.num_q_tokens = num_q_tokens;
+  p.row_cost = tree_row_cost(head_dim);
+  p.segment_cost = tree_segment_cost(head_dim);
   const bool planned = num_seqs > kTreeSelfPlan;
   if (planned) {
     tree_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, ncta);
