@@ -410,10 +410,36 @@ __device__ inline int rank_of(const unsigned long long* v, int n, unsigned long 
   return rank;
 }
 
+// A barrier of the warps that hold segments.
+__device__ inline void select_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSelect) : "memory"); }
+
+// A warp's entries u < N of its lanes for which `take` holds, put at consecutive places
+// from *count on. (By ballots and one atomic: with an atomic an entry the two steps that
+// do this made up 3000 of the join's 12500 cycles.)
+template <int N, typename Take, typename Put>
+__device__ inline void append(int* count, const Take& take, const Put& put) {
+  const unsigned below = (1u << (threadIdx.x & 31)) - 1;
+  unsigned who[N];
+  int total = 0, at = 0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    who[u] = __ballot_sync(0xffffffffu, take(u));
+    total += __popc(who[u]);
+  }
+  if (total == 0) return;
+  if ((threadIdx.x & 31) == 0) at = atomicAdd(count, total);
+  at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    if (who[u] >> (threadIdx.x & 31) & 1) put(u, at + __popc(who[u] & below));
+    at += __popc(who[u]);
+  }
+}
+
 // A CTA per row: a chain of short steps, each with a warp to a scheduler or less, so that
 // it costs what the steps have in instructions (4 to 5 cycles each) and round trips.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_join_kernel(Params p) {
   constexpr int kPer = Vec<T>::kPer;
   __shared__ JoinSmem s;
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -426,7 +452,11 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
     // the row's runs
     const int blocks = (row.end + Vec<T>::kBlock - 1) / Vec<T>::kBlock;
     const int runs = (blocks + p.run_blocks - 1) / p.run_blocks;
-    float m = -INFINITY, S = 0.f, W = 0.f;
+    float m = -INFINITY, S = 0.f, W = 0.f, z = -INFINITY;
+    if (lane == 0 && p.tokens) {
+      const int tok = p.tokens[r];
+      if (tok >= 0 && tok < p.vocab) z = (float)row.base[row.shift + tok];
+    }
     for (int j = lane; j < runs; j += 32) {
       const float4 q = p.part[(long long)i * p.runs + j];
       add_run(m, S, W, q.x, q.y, q.z);
@@ -440,23 +470,25 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
       s.m = all;
       s.lns = lns;
       if (p.entropy) p.entropy[i] = S > 0.f ? fmaxf(lns - kLn2 * (W / S), 0.f) : 0.f;
-      if (p.tokens) {
-        const int tok = p.tokens[r];
-        float z = -INFINITY;
-        if (tok >= 0 && tok < p.vocab) z = (float)row.base[row.shift + tok];
+      if (p.tokens)
         p.logprobs[i] = z > -INFINITY ? (fminf(z, kMaxFinite) - all) - lns : -INFINITY;
-      }
     }
   }
   if (p.top == 0) return;
   // The segments of the `top` largest maxima, the lowest first among equal ones. First a
   // bound that so many reach: of each warp, what a share of its lanes reach.
-  uint32_t key[kSegsPerThread] = {}, mine = 0;
+  // (The runs' warp meets the others after that only.)
   if (warp < kWarps - 1) {
+    uint32_t key[kSegsPerThread] = {}, mine = 0;
 #pragma unroll
     for (int u = 0; u < kSegsPerThread; ++u) {
       const int j = kSelect * u + tid;
       if (j < n) key[u] = ordered(p.seg_max[(long long)i * p.segments + j]);
+    }
+    if (tid < kMaxTop) s.segs[tid] = -1;
+    if (tid == 0) {
+      s.maxima = s.hot = s.count = 0;
+      s.least = -INFINITY;
     }
 #pragma unroll
     for (int u = 0; u < kSegsPerThread; ++u) mine = max(mine, key[u]);
@@ -467,26 +499,20 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
       if (mine == reached) mine = 0;
     }
     if (lane == 0) s.bound[warp] = reached;
-  }
-  if (tid < kMaxTop) s.segs[tid] = -1;
-  if (tid == 0) {
-    s.maxima = s.hot = s.count = 0;
-    s.least = -INFINITY;
-  }
-  __syncthreads();
-  const uint32_t bound = max(min(min(s.bound[0], s.bound[1]), s.bound[2]), 1u);
-  static_assert(kWarps == 4, "bounds of three warps");
-#pragma unroll
-  for (int u = 0; u < kSegsPerThread; ++u)
-    if (key[u] >= bound)                           // (a place without a segment is 0)
-      s.max_key[atomicAdd(&s.maxima, 1)] =
-          (unsigned long long)key[u] << 32 | (uint32_t)~(kSelect * u + tid);
-  __syncthreads();
-  for (int c = tid; c < s.maxima; c += kThreads) {
-    const unsigned long long k = s.max_key[c];
-    const int rank = rank_of(s.max_key, s.maxima, k);
-    if (rank < p.top) s.segs[rank] = (int)~(uint32_t)k;
-    if (rank == p.top - 1 && n > p.top) s.least = unordered((uint32_t)(k >> 32));
+    select_sync();
+    const uint32_t bound = max(min(min(s.bound[0], s.bound[1]), s.bound[2]), 1u);
+    static_assert(kWarps == 4, "bounds of three warps");
+    // (a place without a segment is 0)
+    append<kSegsPerThread>(&s.maxima, [&](int u) { return key[u] >= bound; }, [&](int u, int c) {
+      s.max_key[c] = (unsigned long long)key[u] << 32 | (uint32_t)~(kSelect * u + tid);
+    });
+    select_sync();
+    for (int c = tid; c < s.maxima; c += kSelect) {
+      const unsigned long long k = s.max_key[c];
+      const int rank = rank_of(s.max_key, s.maxima, k);
+      if (rank < p.top) s.segs[rank] = (int)~(uint32_t)k;
+      if (rank == p.top - 1 && n > p.top) s.least = unordered((uint32_t)(k >> 32));
+    }
   }
   __syncthreads();
   const int seg_vecs = p.seg_units * (kUnit / kPer);
@@ -527,12 +553,11 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_join_kernel(Params p) {
       x[u] = Vec<T>::empty();
       if (whole) x[u] = __ldg(reinterpret_cast<const uint4*>(row.base + at[u]));
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (Vec<T>::largest1(x[u]) >= fmaxf(least, -kMaxFinite)) {
-        const int c = atomicAdd(&s.hot, 1);
-        if (c < kHot) s.hot_place[c] = at[u];
-      }
+    append<kBatch>(
+        &s.hot, [&](int u) { return Vec<T>::largest1(x[u]) >= fmaxf(least, -kMaxFinite); },
+        [&](int u, int c) {
+          if (c < kHot) s.hot_place[c] = at[u];
+        });
   }
   __syncthreads();
   // their values, and those of the row's ends (which may lie in other segments)
