@@ -4,15 +4,15 @@
 //   m = max z,  S = sum e^(z - m),  W = sum (z - m) e^(z - m)
 //   log p(v) = z_v - m - ln S       H = ln S - W / S
 //
-// Reading the logits is the floor (HBM); the exponentials are close behind it (one
-// MUFU operation a value, 16 a clock and SM: 131072 values 4.3 us on one SM, against
-// 5.9 us to read them as bf16 at its share of the copy rate), so everything else of a
-// value is kept to a few packed instructions: the maximum is taken on the values as
-// stored, the sums run on pairs, and the reference m is moved only when a block of 512
-// values exceeds it by more than 2^8 (in e^: by 8 ln 2), for the whole warp at once.
+// Reading the logits is the floor (HBM): 1500 rows of 131072 bf16 values 58 us, of which
+// the pass takes 64 and a call 74; 112 rows of 100003 fp32 values 6.6, 9.4 and 20. A value
+// costs the pass 8.7 instructions, which fill 72% of the issue slots: so the maximum is
+// taken on the values as stored, the sums run on pairs, and the reference m is moved only
+// where a block's maximum exceeds it by more than 2^8 (in e^: by 8 ln 2), for the whole
+// warp at once. A block is 1024 values, or 512 of fp32: four 16-byte loads a lane.
 // All sums are fp32, a few thousand terms to a lane before they are merged.
 //
-// The k largest come out of the maxima of segments of 512 values or more, which the
+// The k largest come out of the maxima of segments of 256 values or more, which the
 // pass has anyway: ordered by (maximum, lowest segment first), the k first segments
 // hold the k largest values by (value, lowest index first), since a value of another
 // segment has k values before it. Only those segments are read again, and of them
@@ -20,8 +20,9 @@
 // k segments is read again whole, and the maxima of the threads' shares stand in for
 // the segments'.)
 //
-// Kernel 1: a warp per run of 512-value blocks of a row -> (m, S, W) and the segments'
-// maxima in the workspace. Kernel 2: a CTA per row joins them.
+// Kernel 1: a warp per run of up to 8 blocks of a row -> (m, S, W) and the segments'
+// maxima in the workspace. Kernel 2: a CTA per row joins them. One kernel with a CTA per
+// row took 102 us for the 1500 rows, and one row would have had one SM.
 #include <climits>
 
 #include "splash_common.cuh"
@@ -437,7 +438,11 @@ __device__ inline void append(int* count, const Take& take, const Put& put) {
 }
 
 // A CTA per row: a chain of short steps, each with a warp to a scheduler or less, so that
-// it costs what the steps have in instructions (4 to 5 cycles each) and round trips.
+// it costs what the steps have in instructions (4 to 5 cycles each) and round trips: 3.7 us
+// for one row, 5.5 to 6 for rows of fp32 at odd addresses. The runs' sums (warp 3) are formed
+// beside the selection of the segments: one after the other one row took 0.9 us more. With
+// 16-bit logits ten CTAs an SM, 1500 rows 76.2 -> 73.9 us; fp32 needs the registers for
+// its loads (33 rows 13.4 us at eight, 14.4 at ten).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_join_kernel(Params p) {
   constexpr int kPer = Vec<T>::kPer;

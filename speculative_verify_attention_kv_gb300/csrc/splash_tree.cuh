@@ -32,7 +32,7 @@ constexpr int kTreeTile = 64;
 // 0.93 / 0.0017 / 8.2, of 128 0.63 / 0.0030 / 5.6, of 64 0.57 / 0.0021 / 3.4. Calls, mean
 // us of six ragged batches each at (row, segments in tiles) (6, 6), (6, 9), (14, 6), (14,
 // 9), (19, 9): heads of 256 71.7, 70.7, 73.0, 70.8, 71.9; of 128 55.5, 54.7, 56.5, 54.1,
-// 54.9; of 64 47.6, 48.9, 47.6, 48.6, 48.9. 32 sequences of 1024..32768 keys, heads of
+// 54.9; of 64 47.6, 48.9, 47.6, 48.6, 48.9. 32 sequences of 256..16384 keys, heads of
 // 256: 172 us at (6, 6), 156 at (6, 9), 170 at (6, 20).
 constexpr int kTreeTileCost = 4096;
 __host__ __device__ constexpr int tree_row_cost(int D) { return D > 128 ? 6 : 14; }

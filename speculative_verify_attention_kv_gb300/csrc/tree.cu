@@ -4,7 +4,10 @@
 // A tree of T nodes is an array of parents: node 0 holds the token that the target
 // produced at the step before, parent[t] < t is the node that node t continues, -1
 // has none. Both kernels are chains of dependent steps on a few hundred bytes a
-// tree: latency, not bytes, and so a tree stays in one CTA or one warp.
+// tree: latency, not bytes, and so a tree stays in one CTA or one warp. In a replayed
+// graph (an empty kernel takes 2 us of it) 16 trees of 16 nodes take 4.1 us for the masks
+// and 4.4 for the path, 500 trees of up to 120 nodes 6.2 and 6.2; their bytes would be
+// read and written in 0.001 to 0.12 us.
 #include "splash_common.cuh"
 #include "splash_host.cuh"
 #include "splash_tree.cuh"

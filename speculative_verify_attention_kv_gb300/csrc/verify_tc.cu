@@ -60,6 +60,14 @@
 // bits of its keys from the mask words, once per row and tile, and nothing else
 // of the softmax differs. Only the tiles that hold nodes (5 at most) pay for it.
 // The cut of the stream over the CTAs is computed here, by every CTA for itself.
+// A tile's chain is shorter than above: two converter warps for K and two for V,
+// MMA issuers that run as whole warps with one lane issuing, one barrier that frees
+// a tile's codes and scales (see the roles' comments), and with heads of 64 or 128
+// four S/P buffers and a ring of 8 or 5 stages. 16 sequences of 32768 keys, 16 nodes,
+// 24 query and 4 KV heads: heads of 256 264 us a call (1.12 GB read, 4.3 TB/s; tensor
+// pipe 45%, issue slots 51%), of 128 188 us (32%, 60%), of 64 183 us (17%, 56%). A tile
+// takes 1.1 us, 0.8 and 0.75: a latency, the softmax warps' way from S to P with the
+// waits on both sides, and at heads of 256 the two S/P buffers that tensor memory holds.
 #include <type_traits>
 
 #include "splash_groups.cuh"
@@ -738,13 +746,12 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
 
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // l: this thread's columns
       if constexpr (kTree) {
-        // A softmax warp takes its tiles one after the
-        // other, and with 2 of them a scheduler it is their latency that bounds the kernel
-        // (2230 of the 2270 cycles of a tile at D = 64; 64, 128 and 256 took 241, 245 and
-        // 297 us for the same keys). So the chain of a tile is kept short: the running
-        // maximum is looked at by each thread for its own keys, and only where one passes
-        // it by more than 2^8 is it reduced over the row and moved, with O and the sums
-        // (the same decisions as a reduction every tile would take).
+        // A softmax warp takes its tiles one after the other, and with 2 of them a
+        // scheduler their latency bounds the kernel. So the chain of a tile is kept short:
+        // the running maximum is looked at by each thread for its own keys, and only where
+        // one passes it by more than 2^8 is it reduced over the row and moved, with O and
+        // the sums (the same decisions as a reduction every tile would take; 306 -> 285 us
+        // for 16 x 32768 keys).
         float base[2] = {0.f, 0.f};
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // base: rowfac * (running maximum); limit: the x that moves it
