@@ -85,6 +85,7 @@ constexpr int kLoadWarps = 4;
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;   // TMEM allocation, QK issue (even tiles)
 constexpr int kQkOddWarp = kMmaWarp + 1;                // QK issue (odd tiles)
+constexpr int kScaleWarp = kQkOddWarp;                  // trees: scales and prefetch instead
 constexpr int kPvWarp = kQkOddWarp + 1;                 // PV issue
 constexpr int kProducerWarp = kPvWarp + 1;
 // 16 warps = 4 per SM sub-partition, so each thread may hold 128 registers
@@ -353,6 +354,14 @@ __device__ __forceinline__ int stage_codes(const AttnParams& p, const Seg& s, in
   return page;
 }
 
+// The id of page (lane & 3) of tile `it` as stage_codes takes it (trees).
+__device__ __forceinline__ int tile_page(const AttnParams& p, const Seg& s, int it, int lane,
+                                         PageWindow& win) {
+  const int page = win.get(p, s.b, it * kPagesPerTile, (s.Lk + kPageSize - 1) / kPageSize, lane);
+  const bool needed = it * kTileKeys + kPageSize * (lane & 3) < s.Lk;
+  return needed && page < p.num_pages ? page : -1;
+}
+
 // Producer: the tile's K and V scales, 16 bytes per lane by cp.async (lanes
 // 0..15 K, 16..31 V; page (lane & 15) / 4, slots 4 * (lane & 3) ..); each
 // lane's arrival on the scale barrier fires when its copy has landed.
@@ -537,10 +546,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(smem_u32(&sh->ring_full[s]), 1);
-      // trees: ring_empty[0] alone, for the codes and the scales of the tile
-      for (int kv = 0; kv < 2; ++kv)
-        mbar_init(smem_u32(&sh->ring_empty[kv][s]),
-                  kTree ? kLoadWarps + kSoftmaxWarps : kLoadWarps);
+      // (trees: ring_empty[0] alone, two converter warps a half of the stage)
+      for (int kv = 0; kv < 2; ++kv) mbar_init(smem_u32(&sh->ring_empty[kv][s]), kLoadWarps);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh->k_full[s]), kConvertWarps);
@@ -558,7 +565,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       mbar_init(smem_u32(&sh->v_full[s]), kConvertWarps);
     }
     mbar_init(smem_u32(&sh->q_full), kSoftmaxWarps);
-    mbar_init(smem_u32(&sh->q_ack), 2);
+    mbar_init(smem_u32(&sh->q_ack), kTree ? 1 : 2);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&sh->drain[i]), 1);
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -893,7 +900,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&sh->p_full[st]));
-            mbar_arrive(smem_u32(&sh->ring_empty[0][sst]));  // the scales are read
+            mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
           }
           if (++sst == kScStages) sst = 0, sc_phase ^= 1;
         }
@@ -1196,6 +1203,31 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       }
     }
     }
+  } else if (kTree && warp == kScaleWarp) {
+    // ================================================ scales and prefetch (trees)
+    // Beside the codes' producer, which has 2000 cycles of work a tile with both: 264 ->
+    // XXX us for 16 x 32768 keys, heads of 256.
+    if constexpr (kTree) {
+      int g = 0;
+      Seg s;
+      bool ok = true;
+      PageWindow win;
+      while (ok && iter.next(s)) {
+        for (int it = s.i0; it < s.i1; ++it, ++g) {
+          const int r = g % kRing;
+          if (lane == 0) ok = sync.wait(smem_u32(&sh->sc_free[r]), ((g / kRing) & 1) ^ 1);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          stage_scales(p, s, tile_page(p, s, it, lane, win), scales + r * 2 * kTileKeys,
+                       smem_u32(&sh->sc_full[r]), lane);
+          if constexpr (C::kPrefetch) {
+            const int ahead = it + kRing;
+            prefetch_tile<D>(p, s, ahead, win.peek(s.b, ahead * kPagesPerTile + (lane & 3)), lane);
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
   } else if (warp >= kProducerWarp) {
     // ============================================================ producer
     int g = 0, armed = 0;                                   // armed: tiles staged so far
@@ -1216,13 +1248,13 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         const int page = stage_codes<D>(p, s, it, stage, smem_u32(&sh->ring_full[r]), lane, win);
-        stage_scales(p, s, page, scales + sst * 2 * kTileKeys, smem_u32(&sh->sc_full[sst]), lane);
         ++armed;
+        if constexpr (kTree) continue;                      // the rest is kScaleWarp's
+        stage_scales(p, s, page, scales + sst * 2 * kTileKeys, smem_u32(&sh->sc_full[sst]), lane);
         // The codes of the tile kRing ahead into L2 only (no shared memory): its
         // staging copy, issued when this ring stage frees again, then hits L2.
         // Measured 5-6% faster on 16 x 32K and the ragged batch; 2 to 4 tiles
-        // ahead do the same, 6 less. (For trees, on the PV issuer's warp instead: 274
-        // -> 292 to 325 us.)
+        // ahead do the same, 6 less.
         if constexpr (C::kPrefetch) {
           const int ahead = it + kRing;
           prefetch_tile<D>(p, s, ahead, win.peek(s.b, ahead * kPagesPerTile + (lane & 3)), lane);
@@ -1255,12 +1287,12 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       const uint64_t kdesc0 = sdesc(smem_u32(kbuf), 16, 1024);
       const uint64_t vdesc0 = sdesc(smem_u32(vbuf), kTileKeys * 128, 1024);
       const bool leader = elect_one();
-      const int role = warp - kMmaWarp;             // 0, 1: QK of even, odd tiles; 2: PV
+      const int role = warp - kMmaWarp;             // 0: QK of every tile; 2: PV
       int g = 0, nsegs = 0;
       Seg s;
       bool ok = true;
       while (ok && iter.next(s)) {
-        if (role < 2) {
+        if (role == 0) {
           ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->q_full), nsegs & 1));
           if (!ok) break;
           fence_after();
@@ -1268,8 +1300,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         }
         for (int it = s.i0; it < s.i1; ++it, ++g) {
           const int st = g % kStages;
-          if (role < 2) {
-            if (st % 2 != role) continue;
+          if (role == 0) {
             ok = sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1) &&
                  sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1);
             ok = __all_sync(0xffffffffu, ok);
