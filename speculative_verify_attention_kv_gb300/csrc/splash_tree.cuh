@@ -33,7 +33,9 @@ constexpr int kTreeTile = 64;
 // us of six ragged batches each at (row, segments in tiles) (6, 6), (6, 9), (14, 6), (14,
 // 9), (19, 9): heads of 256 71.7, 70.7, 73.0, 70.8, 71.9; of 128 55.5, 54.7, 56.5, 54.1,
 // 54.9; of 64 47.6, 48.9, 47.6, 48.6, 48.9. 32 sequences of 256..16384 keys, heads of
-// 256: 172 us at (6, 6), 156 at (6, 9), 170 at (6, 20).
+// 256: 172 us at (6, 6), 156 at (6, 9), 170 at (6, 20). (With the kernel as it is now
+// tiles are 5% shorter and six batches of heads of 256 take 69.9, 67.3 and 67.6 us at
+// (14, 6), (6, 9) and (14, 9): the same order.)
 constexpr int kTreeTileCost = 4096;
 __host__ __device__ constexpr int tree_row_cost(int D) { return D > 128 ? 6 : 14; }
 __host__ __device__ constexpr int tree_segment_cost(int D) { return (D > 64 ? 9 : 6) * 4096; }

@@ -60,14 +60,14 @@
 // bits of its keys from the mask words, once per row and tile, and nothing else
 // of the softmax differs. Only the tiles that hold nodes (5 at most) pay for it.
 // The cut of the stream over the CTAs is computed here, by every CTA for itself.
-// A tile's chain is shorter than above: two converter warps for K and two for V,
-// MMA issuers that run as whole warps with one lane issuing, one barrier that frees
-// a tile's codes and scales (see the roles' comments), and with heads of 64 or 128
-// four S/P buffers and a ring of 8 or 5 stages. 16 sequences of 32768 keys, 16 nodes,
-// 24 query and 4 KV heads: heads of 256 264 us a call (1.12 GB read, 4.3 TB/s; tensor
-// pipe 45%, issue slots 51%), of 128 188 us (32%, 60%), of 64 183 us (17%, 56%). A tile
-// takes 1.1 us, 0.8 and 0.75: a latency, the softmax warps' way from S to P with the
-// waits on both sides, and at heads of 256 the two S/P buffers that tensor memory holds.
+// The roles differ in places, for a shorter chain and a ring that is free sooner: two
+// converter warps for K and two for V, one warp for all QK issues, warp 13 for the
+// scales and the prefetch, MMA issuers that run as whole warps with one lane issuing,
+// an S barrier that stands for the tile's scales too, and with heads of 64 or 128 four
+// S/P buffers and a ring of 8 or 5 stages. 16 sequences of 32768 keys, 16 nodes, 24
+// query and 4 KV heads: heads of 256 246 us a call (1.12 GB read, 4.7 TB/s in the
+// kernel), of 128 180 us, of 64 175 us. A tile takes 1.0, 0.75 and 0.7 us: a latency,
+// the softmax warps' way from S to P with the waits on both sides.
 #include <type_traits>
 
 #include "splash_groups.cuh"
@@ -552,7 +552,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh->k_full[s]), kConvertWarps);
       mbar_init(smem_u32(&sh->k_free[s]), 1);
-      mbar_init(smem_u32(&sh->s_full[s]), 1);
+      mbar_init(smem_u32(&sh->s_full[s]), kTree ? 2 : 1);
       mbar_init(smem_u32(&sh->p_full[s]), kSoftmaxWarps);
       mbar_init(smem_u32(&sh->p_free[s]), 1);
     }
@@ -636,7 +636,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     int g = 0, nsegs = 0;
     Seg s;
     bool ok = true;
-    uint32_t sst = 0, sc_phase = 0;                       // trees: tile g % kScStages, (g / kScStages) & 1
+    uint32_t sst = 0;                                     // trees: tile g % kScStages
     while (ok && iter.next(s)) {
       // Q' of this segment overwrites the previous one: both QK issuers must
       // have seen the previous q_full phase (so neither lags it by two phases)
@@ -765,20 +765,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         float limit[2] = {-INFINITY, -INFINITY};
         for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
           const int st = g % kStages;
-          // what need not follow S comes before the wait for it: the tile's scales
+          // (the QK issuer has waited for the tile's scales)
           const float* ks = scales + sst * 2 * kTileKeys;
           const float* vs = ks + kTileKeys;
-          float2 ks2[8];
-          ok = sync.wait(smem_u32(&sh->sc_full[sst]), sc_phase);
-          if (warp_live && ok) {
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-              const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
-              ks2[2 * i4] = make_float2(kq.x, kq.y);
-              ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
-            }
-          }
-          ok = ok && sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1);
+          ok = sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;                                   // a timeout seen by some lanes
           fence_after();
@@ -787,7 +777,13 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             uint32_t sv[32];
             tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
             const int k0 = it * kTileKeys;
-            float2 x[2][8];
+            float2 x[2][8], ks2[8];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
+              ks2[2 * i4] = make_float2(kq.x, kq.y);
+              ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
+            }
             tmem_wait_ld(sv);         // sv is read only after the wait
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -902,7 +898,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             mbar_arrive(smem_u32(&sh->p_full[st]));
             mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
           }
-          if (++sst == kScStages) sst = 0, sc_phase ^= 1;
+          if (++sst == kScStages) sst = 0;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -1205,8 +1201,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     }
   } else if (kTree && warp == kScaleWarp) {
     // ================================================ scales and prefetch (trees)
-    // Beside the codes' producer, which has 2000 cycles of work a tile with both: 264 ->
-    // XXX us for 16 x 32768 keys, heads of 256.
+    // Beside the codes' producer, which has 2000 cycles of work a tile with both: with
+    // the codes' stages freed by the converters alone 264 -> 245 us for 16 x 32768 keys,
+    // heads of 256. (On the PV issuer's warp the prefetch cost 18 to 50 us more; two to five
+    // tiles further ahead 245, 247, 254; left with the codes 251.)
     if constexpr (kTree) {
       int g = 0;
       Seg s;
@@ -1301,7 +1299,15 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         for (int it = s.i0; it < s.i1; ++it, ++g) {
           const int st = g % kStages;
           if (role == 0) {
-            ok = sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1) &&
+            // S and the tile's scales together: the softmax has one wait less (heads of 128
+            // 191 -> 180 us for 16 x 32768 keys). With two S/P buffers this warp is in the
+            // chain, so there the scales' wait comes after the issue (252 -> 246 us at
+            // heads of 256; heads of 128 180 -> 183).
+            const auto scales_there = [&] {
+              return sync.wait(smem_u32(&sh->sc_full[g % kScStages]), (g / kScStages) & 1);
+            };
+            ok = (!C::kDeep || scales_there()) &&
+                 sync.wait(smem_u32(&sh->k_full[st]), (g / kStages) & 1) &&
                  sync.wait(smem_u32(&sh->p_free[st]), ((g / kStages) & 1) ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -1316,6 +1322,11 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
               mma_commit(smem_u32(&sh->s_full[st]));
               mma_commit(smem_u32(&sh->k_free[st]));
             }
+            if constexpr (!C::kDeep) {
+              ok = __all_sync(0xffffffffu, scales_there());
+              if (!ok) break;
+            }
+            if (leader) mbar_arrive(smem_u32(&sh->s_full[st]));
           } else {
             ok = sync.wait(smem_u32(&sh->v_full[st]), (g / kStages) & 1) &&
                  sync.wait(smem_u32(&sh->p_full[st]), (g / kStages) & 1);
