@@ -1278,8 +1278,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     // write after an earlier MMA's read).
     // warp kPvWarp: PV(i) into O once the softmax has written P(i).
     if constexpr (kTree) {
-      // the warp as one, so that addresses and descriptors can stay uniform; one lane
-      // issues
+      // kMmaWarp issues the QK of every tile. The warp as one, so that addresses and
+      // descriptors can stay uniform; one lane issues
       constexpr uint32_t kIdescQK = idesc_f16(128, kTileKeys, 0, 0);
       constexpr uint32_t kIdescPV = idesc_f16(128, D, 0, 1);
       const uint64_t kdesc0 = sdesc(smem_u32(kbuf), 16, 1024);
