@@ -1206,6 +1206,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     // heads of 256. (On the PV issuer's warp the prefetch cost 18 to 50 us more; two to five
     // tiles further ahead 245, 247, 254; left with the codes 251.)
     if constexpr (kTree) {
+      static_assert(kScStages == kRing, "scale stages");
       int g = 0;
       Seg s;
       bool ok = true;
