@@ -13,7 +13,7 @@
 // whole or in parts. The combine goes by the list of shared units, of which there are
 // fewer than CTAs: looking up every output row's unit in the plan instead made it 25
 // us of a 218 us call (32 ragged sequences, 1,000 nodes, 24 heads of 256), this way it
-// is 11 of 155. What is left of it is the launch and three loads one after the other
+// is 12 of 154. What is left of it is the launch and three loads one after the other
 // (list, lse, rows) before the sums.
 #include <climits>
 
