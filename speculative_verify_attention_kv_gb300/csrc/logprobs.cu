@@ -44,6 +44,8 @@ constexpr int kHot = 256, kCandidates = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kMaxFinite = 3.402823466e38f;
 constexpr float kMoveLog2 = 8.0f;
+constexpr float kNear = 65536.f;         // references that one fused product a value is right for
+constexpr float kNothing = -200.f;       // 2^ this and less is 0 in fp32
 
 struct Params {
   const void* logits;
@@ -220,27 +222,49 @@ __device__ inline int out_row(const Params& p, int i) {
   return r;
 }
 
+// (S, W) with every exponent d larger.
+__device__ inline void shift_exponents(float d, float& S, float& W) {
+  const float f = ex2(d);
+  W = f * (W + d * S);
+  S *= f;
+}
+
 // Moves (S, W) from reference m to m2.
 __device__ inline void move_reference(float m, float m2, float& S, float& W) {
   if (m == -INFINITY) {                  // nothing summed yet
     S = W = 0.f;
     return;
   }
-  const float d = fmaxf((m - m2) * kLog2e, -2000.f), f = ex2(d);
-  W = f * (W + d * S);
-  S *= f;
+  shift_exponents(fmaxf((m - m2) * kLog2e, -2000.f), S, W);
 }
 
-// What a warp has summed: S and W as pairs that are added up at the end.
+// What a warp has summed: S and W as pairs that are added up at the end. With a
+// reference near 0 an exponent is one fused product, z log2 e + shift, where shift is
+// -m log2 e rounded: every exponent is too large by `rest`, what the rounding cut off,
+// and the sums' are made good once, when the reference moves or the run ends. (Left in, it
+// is 6e-4 of log p at a logit of 30000, and at 1e10 no weight is anywhere near its value.)
+// Beyond kNear rest would grow: there the maximum is taken off first, at an instruction
+// more a pair, and rest is 0.
 struct Sums {
   float m = -INFINITY;                   // the same in every lane
+  float shift = 0.f, rest = 0.f;
   float2 S = make_float2(0.f, 0.f), W = make_float2(0.f, 0.f);
-  __device__ void refer_to(float m2) {
+  __device__ bool near() const { return fabsf(m) <= kNear; }
+  // The sums about their reference itself.
+  __device__ float2 plain() const {
     float s = S.x + S.y, w = W.x + W.y;
-    move_reference(m, m2, s, w);
-    S = make_float2(s, 0.f);
-    W = make_float2(w, 0.f);
+    shift_exponents(-rest, s, w);
+    return make_float2(s, w);
+  }
+  __device__ void refer_to(float m2) {
+    float2 a = plain();
+    move_reference(m, m2, a.x, a.y);
     m = m2;
+    shift = -__fmul_rn(m, kLog2e);
+    rest = near() ? __fmaf_rn(m, kLog2e, shift) : 0.f;
+    shift_exponents(rest, a.x, a.y);
+    S = make_float2(a.x, 0.f);
+    W = make_float2(a.y, 0.f);
   }
 };
 
@@ -266,7 +290,7 @@ __device__ inline void block_by_value(const Row<T>& row, int b, Sums& a,
 #pragma unroll
     for (int u = 0; u < kUnit / 32; ++u) {
       if (!(z[u] > -INFINITY)) continue;           // NaN neither
-      const float t = fmaxf((fminf(z[u], kMaxFinite) - a.m) * kLog2e, -2000.f), e = ex2(t);
+      const float t = fmaxf((fminf(z[u], kMaxFinite) - a.m) * kLog2e, -2000.f) + a.rest, e = ex2(t);
       a.S.x += e;
       a.W.x += e * t;
     }
@@ -341,14 +365,16 @@ __device__ inline float3 run_over(const Row<T>& row, int b0, int b1, int seg_uni
 #pragma unroll
     for (int g = 1; g < kUnits; ++g) top = fmaxf(top, unit[g]);
     note(unit, top, b + 1 == b1);
+    const float above = (top - a.m) * kLog2e;
+    if (above < kNothing) continue;      // weights of 0, as a mask's values have
     if (!(top > Vec<T>::kFast && fmaxf(top, a.m) < 1e37f)) {
       if (top > -INFINITY) block_by_value(row, b, a, unit);
       continue;
     }
-    if (!((top - a.m) * kLog2e <= kMoveLog2)) a.refer_to(top);
+    if (!(above <= kMoveLog2)) a.refer_to(top);
     const float2 scale = make_float2(kLog2e, kLog2e);
-    const float2 shift = make_float2(-a.m * kLog2e, -a.m * kLog2e);
-    if (!careful) {
+    if (!careful && a.near()) {
+      const float2 shift = make_float2(a.shift, a.shift);
       const float2 S0 = a.S, W0 = a.W;
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
@@ -360,17 +386,18 @@ __device__ inline float3 run_over(const Row<T>& row, int b0, int b1, int seg_uni
           a.W = __ffma2_rn(e, t, a.W);
         }
       // a value of -inf (or near it, or NaN) has made W NaN: this block again, and
-      // the rest of the run, with such values raised
+      // the rest of the run, with such values raised (S stays finite: t <= 8)
       careful = __any_sync(0xffffffffu, !(a.W.x + a.W.y == a.W.x + a.W.y));
       if (!careful) continue;
       a.S = S0;
       a.W = W0;
     }
+    const float2 minus = make_float2(-a.m, -a.m), rest = make_float2(a.rest, a.rest);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
 #pragma unroll
       for (int k = 0; k < kPer / 2; ++k) {
-        const float2 t = __ffma2_rn(Vec<T>::raised(x[u], k), scale, shift);
+        const float2 t = __ffma2_rn(__fadd2_rn(Vec<T>::raised(x[u], k), minus), scale, rest);
         const float2 e = make_float2(ex2(t.x), ex2(t.y));
         a.S = __fadd2_rn(a.S, e);
         a.W = __ffma2_rn(e, t, a.W);
@@ -378,7 +405,8 @@ __device__ inline float3 run_over(const Row<T>& row, int b0, int b1, int seg_uni
   }
 #pragma unroll 1
   for (int b = in1; b < b1; ++b) edge(b);
-  return make_float3(a.m, warp_sum(a.S.x + a.S.y), warp_sum(a.W.x + a.W.y));
+  const float2 q = a.plain();
+  return make_float3(a.m, warp_sum(q.x), warp_sum(q.y));
 }
 
 // Adds a run to (m, S, W).
@@ -391,6 +419,11 @@ __device__ inline void add_run(float& m, float& S, float& W, float m2, float S2,
   }
   S += S2;
   W += W2;
+}
+
+// ln p of a value, which rounding does not take above 0.
+__device__ inline float log_p(float z, float m, float lns) {
+  return fminf((fminf(z, kMaxFinite) - m) - lns, 0.f);
 }
 
 struct JoinSmem {
@@ -476,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_jo
       s.lns = lns;
       if (p.entropy) p.entropy[i] = S > 0.f ? fmaxf(lns - kLn2 * (W / S), 0.f) : 0.f;
       if (p.tokens)
-        p.logprobs[i] = z > -INFINITY ? (fminf(z, kMaxFinite) - all) - lns : -INFINITY;
+        p.logprobs[i] = z > -INFINITY ? log_p(z, all, lns) : -INFINITY;
     }
   }
   if (p.top == 0) return;
@@ -583,9 +616,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_jo
   __syncthreads();
   const int count = s.count;
   const auto put = [&](int rank, unsigned long long k) {
-    const float z = fminf(unordered((uint32_t)(k >> 32)), kMaxFinite);
     p.top_ids[(long long)i * p.top + rank] = (int32_t)~(uint32_t)k;
-    p.top_logprobs[(long long)i * p.top + rank] = (z - s.m) - s.lns;
+    p.top_logprobs[(long long)i * p.top + rank] =
+        log_p(unordered((uint32_t)(k >> 32)), s.m, s.lns);
   };
   if (hot <= kHot && count <= kCandidates) {
     for (int c = tid; c < count; c += kThreads) {
