@@ -716,8 +716,9 @@ int splash_accept_tree(const int32_t* block_tokens, const int32_t* parents,
  *   numbers. code_layer_stride is a multiple of 16, both at least a pool's size.
  * A path row before o + i or outside the sequence reports SPLASH_DEVICE_BAD_TREE, a
  * slot past the pool SPLASH_DEVICE_BAD_PAGE; that row is not moved, nor one with a
- * negative slot. An accepted count past the sequence's rows reports
- * SPLASH_DEVICE_BAD_LENGTH and moves nothing of it. The slots of a call differ.
+ * negative slot. Unusable offsets, whatever the count, and an accepted count past the
+ * sequence's rows report SPLASH_DEVICE_BAD_LENGTH and move nothing of it. The slots of a
+ * call differ.
  */
 int splash_kv_compact(int8_t* k_pages, int8_t* v_pages, float* k_scales, float* v_scales,
                       long long code_layer_stride, long long scale_layer_stride, int num_layers,

@@ -63,11 +63,11 @@ __global__ void __launch_bounds__(kThreads, 8) kv_compact_kernel(CompactParams p
     dst = p.slots[first + 1 + lane];
   }
   const int accepted = p.accepted[b];
-  if (accepted <= 0) return;                     // the root is where it belongs
-  if (!usable || accepted >= end - first) {
+  if (!usable || (accepted > 0 && accepted >= end - first)) {
     if (lane == 0) report(p.status, SPLASH_DEVICE_BAD_LENGTH);
     return;
   }
+  if (accepted <= 0) return;                     // the root is where it belongs
   const int count = accepted + 1;
   for (int base = 1; base < count; base += 32) {
     const int i = base + lane;
