@@ -94,6 +94,23 @@ static_assert(kThreads == 512, "warp roles");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;          // lazy rescale threshold (factor 256)
 
+// The products p * s_V are rounded to fp16 on their way to the second MMA. V scales are
+// about 0.01, so that a weight below 2^-8 of the largest would already lose bits there and
+// one below 2^-18 be nothing: with a sink that holds most of the weight that is much of
+// the output. So a row's weights carry a power of two f that puts the largest V scale it
+// has seen at 2^5 <= f s_V < 2^7 (p * f * s_V < 2^15, which leaves the reference's rounding
+// a factor of two). It is chosen with the row's first key, lowered where a larger scale
+// comes, and cancels in O / l. A row holds 127 / f, the largest scale that f still serves.
+// (f stays within 2^-96 .. 2^64, so that sums of weights stay normal fp32 numbers: below
+// V scales of 2^-59 products get small again, above 2^103 they overflow.)
+__device__ __forceinline__ float v_top_for(float scale) {
+  const int e = 132 - (int)(__float_as_uint(scale) >> 23);       // f = 2^e, f * scale in [32, 64)
+  return __uint_as_float((uint32_t)(133 - max(-96, min(64, e))) << 23 | 0x7e0000u);
+}
+__device__ __forceinline__ int v_factor_log2(float v_top) {
+  return 133 - (int)(__float_as_uint(v_top) >> 23);
+}
+
 // Trees with heads of 64 or 128 have room for more of everything, which takes the wait
 // for a buffer out of the chain QK -> softmax -> PV -> QK, and for a ring so deep that
 // no prefetch has to run ahead of it.
@@ -506,6 +523,26 @@ __device__ __forceinline__ void convert_codes_fast(const uint8_t* src, uint8_t* 
   }
 }
 
+// The largest of 16 keys' V scales among those that two rows see (bits m0 and m1), for a
+// tile with nodes: a masked key's scale may be anything, and is not to touch f. Called
+// where f is chosen or lowered only, and out of line: inlined it cost the whole loop
+// registers (32 ragged sequences 155 -> 165 us, heads of 128 180 -> 191; like this 155
+// and 186).
+__device__ __noinline__ float2 largest_seen(const float* vs, int quad, uint32_t m0, uint32_t m1) {
+  float v[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i4 = 0; i4 < 4; ++i4) {
+    const float4 q4 = *reinterpret_cast<const float4*>(vs + 16 * quad + 4 * (i4 ^ quad));
+    const float w[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (m0 >> (4 * i4 + i) & 1) v[0] = fmaxf(v[0], fabsf(w[i]));
+      if (m1 >> (4 * i4 + i) & 1) v[1] = fmaxf(v[1], fabsf(w[i]));
+    }
+  }
+  return make_float2(v[0], v[1]);
+}
+
 // ------------------------------------------------------------------- kernel
 // kSwa: sliding-window instantiation (window read from the parameters); the
 // plain one compiles the window bounds out. kItems: the plan holds prefix
@@ -752,6 +789,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       warp_arrive(smem_u32(&sh->q_full), lane);
 
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // l: this thread's columns
+      float down[2] = {1.f, 1.f};                         // 1 / f
       if constexpr (kTree) {
         // A softmax warp takes its tiles one after the other, and with 2 of them a
         // scheduler their latency bounds the kernel. So the chain of a tile is kept short:
@@ -761,8 +799,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // for 16 x 32768 keys).
         float base[2] = {0.f, 0.f};
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // base: rowfac * (running maximum); limit: the x that moves it
+        // base: rowfac * (running maximum) - log2 f; limit: the x that moves it; v_top: the V
+        // scale that lowers f
         float limit[2] = {-INFINITY, -INFINITY};
+        float v_top[2] = {127.f, 127.f}, v_low = 127.f;
         for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
           const int st = g % kStages;
           // (the QK issuer has waited for the tile's scales)
@@ -778,6 +818,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
             const int k0 = it * kTileKeys;
             float2 x[2][8], ks2[8];
+            // two of the tile's V scales in a lane, all 64 in the warp
+            const float2 vq2 = *reinterpret_cast<const float2*>(
+                vs + 16 * quad + 4 * ((lane >> 3) ^ quad) + 2 * (lane >> 2 & 1));
+            const float vt = fmaxf(fabsf(vq2.x), fabsf(vq2.y));
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
               const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
@@ -821,19 +865,41 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
 #pragma unroll
               for (int i = 0; i < 8; ++i) mt[k] = fmax3(mt[k], x[k][i].x, x[k][i].y);
             }
-            if (__any_sync(0xffffffffu, mt[0] > limit[0] || (k1_live && mt[1] > limit[1]))) {
+            if (__any_sync(0xffffffffu, vt > v_low || mt[0] > limit[0] ||
+                                            (k1_live && mt[1] > limit[1]))) {
+              // the largest V scale that a row sees: of a tile with nodes the row's own
+              float v[2];
+              v[0] = v[1] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vt)));
+              if (k0 + kTileKeys > s.ctx) {
+                const float2 own = largest_seen(vs, quad, vm[0], vm[1]);
+                v[0] = own.x;
+                v[1] = own.y;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 1));
+                  v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 2));
+                }
+              }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 float t = mt[k];
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                if (t > limit[k]) {                          // the same in the row's threads
-                  alpha[k] = limit[k] == -INFINITY ? 0.f : ex2(base[k] - rowfac[k] * t);
-                  base[k] = rowfac[k] * t;
-                  limit[k] = t + kRescaleLog2 / rowfac[k];
+                const bool first = limit[k] == -INFINITY, moves = t > limit[k];
+                if (first ? moves : moves || v[k] > v_top[k]) {  // the same in the row's threads
+                  float ref = base[k] + (float)v_factor_log2(v_top[k]);
+                  if (moves) {
+                    ref = rowfac[k] * t;
+                    limit[k] = t + kRescaleLog2 / rowfac[k];
+                  }
+                  if (first || v[k] > v_top[k]) v_top[k] = v_top_for(v[k]);
+                  ref -= (float)v_factor_log2(v_top[k]);
+                  alpha[k] = first ? 0.f : ex2(base[k] - ref);
+                  base[k] = ref;
                   sum[k] = make_float2(sum[k].x * alpha[k], sum[k].y * alpha[k]);
                 }
               }
+              v_low = k1_live ? fminf(v_top[0], v_top[1]) : v_top[0];
             }
             float2 vs2[8];
 #pragma unroll
@@ -902,7 +968,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          m[k] = base[k];                                 // rowfac * m
+          m[k] = base[k] + (float)v_factor_log2(v_top[k]);   // rowfac * m
+          down[k] = __uint_as_float((uint32_t)(127 - v_factor_log2(v_top[k])) << 23);
           l[k] = sum[k].x + sum[k].y;
           // the row again, from what was kept of it
           live[k] = rr[k] >= 0;
@@ -1123,7 +1190,8 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           if (live[k] && quad == 0) {
             const float lse =
                 l[k] > 0.f
-                    ? ((kTree ? m[k] : rowfac[k] * m[k]) + __log2f(l[k])) * 0.69314718055994531f
+                    ? ((kTree ? m[k] : rowfac[k] * m[k]) + __log2f(l[k] * down[k])) *
+                          0.69314718055994531f
                     : -INFINITY;
             if (ns == 1) p.lse[qrow_off[k]] = lse;
             else lse_part[prow[k]] = lse;

@@ -1,0 +1,128 @@
+"""Attention where one key holds most of the weight and its own value is small, so that the
+output is what the others add, against the fp64 oracle.
+
+Bounds as in test_gpu_tree_attention.py but for the products p s_V that are rounded to
+fp16: they carry a power of two f that puts the largest V scale of the keys that a row
+sees, M, at 2^5 <= f M < 2^7. So a subnormal product is off by 2^-25 / f <= M 2^-30, times a
+code of at most 127, for n keys: n 127 M 2^-30 / S.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from oracle import tree_oracle as T  # noqa: E402
+
+from test_gpu_tree_attention import Case  # noqa: E402
+
+
+class Sink(Case):
+    """Key `at` of every sequence has a score about `gap` above the others' (in e^: so many
+    times their weight) and a value `small` times theirs; V scales `unit` times 0.5 to 1,
+    and `growth` times that from key `grows` on."""
+
+    def __init__(self, seed, ctx, lens, hq, hkv, D, gap, at=0, small=0.0, unit=0.01, grows=None,
+                 growth=1.0, kind="tree"):
+        super().__init__(seed, ctx, lens, hq, hkv, D, kind=kind)
+        rng = np.random.default_rng(seed + 1)
+        u = rng.choice([-1.0, 1.0], (hkv, D))
+        q = 0.5 * np.repeat(u, hq // hkv, 0)[None] + 0.05 * rng.standard_normal((self.n, hq, D))
+        self.q = torch.tensor(q, dtype=torch.bfloat16, device="cuda")
+        self.scales[0] *= 0.01                          # the others' scores: next to nothing
+        for b in range(len(ctx)):
+            for j in range(ctx[b] + lens[b]):
+                pg, s = self.table[b, j // 16], j % 16
+                self.scales[1, pg, :, s] *= unit / 0.01 * (growth if grows and j >= grows else 1)
+            pg, s = self.table[b, at // 16], at % 16
+            self.codes[pg, :, 0, s] = (100 * u).astype(np.int8)
+            self.scales[0, pg, :, s] = gap / (self.sm * 100 * 0.5 * D)
+            self.scales[1, pg, :, s] = unit * small
+        codes = torch.tensor(self.codes, device="cuda")
+        self.pool.k_codes, self.pool.v_codes = self.codes[:, :, 0], self.codes[:, :, 1]
+        self.pool.k_scales, self.pool.v_scales = self.scales[0], self.scales[1]
+        self.dev = (codes[:, :, 0], codes[:, :, 1], torch.tensor(self.scales[0], device="cuda"),
+                    torch.tensor(self.scales[1], device="cuda"))
+        self.want = None
+
+    def check(self, out, lse, rows=slice(None)):
+        if self.want is None:
+            self.want = T.attention(self.q.double().cpu().numpy(), self.pool, self.table, self.ctx,
+                                    self.lens, self.masks, self.hkv, self.sm)
+        want, wl, (av, qk, total) = self.want
+        o, got = out[:self.n].double().cpu().numpy(), lse[:self.n].double().cpu().numpy()
+        keys = max(c + t for c, t in zip(self.ctx, self.lens))
+        M = max(self.scales[1, self.table[b, j // 16], :, j % 16].max()
+                for b in range(len(self.ctx)) for j in range(self.ctx[b] + self.lens[b]))
+        d = 2 * (self.D + 8) * 2.0 ** -24 * qk + 2.0 ** -21
+        live = ~np.isneginf(wl)
+        assert np.array_equal(np.isneginf(got), ~live) and not o[~live].any()
+        off = np.abs(got - wl)[live]
+        assert (off <= (d + 2.0 ** -21)[live] + 2.0 ** -22 * np.abs(wl[live])).all(), off.max()
+        bound = 2.0 ** -8 * np.abs(want) + (2 * d[..., None] + 2.0 ** -11) * av \
+            + (keys * 127 * M * 2.0 ** -30 / total)[..., None]
+        err = np.abs(o - want)
+        assert (err <= bound)[live].all(), (err / np.maximum(bound, 1e-30))[live].max()
+
+
+GAPS = [6.0, 9.0, 12.0, 16.0]                 # the sink's weight: 0.2 to 0.9999 of a row's
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", GAPS)
+@pytest.mark.parametrize("at", [0, 1500])
+def test_trees_keep_small_weights(D, gap, at):
+    c = Sink(41, [2000, 1700], [9, 40], 4, 2, D, gap, at, small=0.02)
+    for ctas in (1, 3, 0):
+        c.check(*c.run(ctas=ctas))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("unit", [1e-6, 1e-3, 1.0, 1e3, 1e6, 1e30])
+def test_trees_at_any_size_of_the_values(D, unit):
+    c = Sink(42, [700], [20], 4, 1, D, 9.0, small=0.02, unit=unit)
+    for ctas in (1, 0):
+        c.check(*c.run(ctas=ctas))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("growth", [3.0, 300.0, 1e7, 1e-4])
+@pytest.mark.parametrize("grows", [33, 200, 701])
+def test_trees_whose_values_grow_along_the_keys(D, growth, grows):
+    """From inside the first tile, the context's middle and the tree's nodes on."""
+    c = Sink(43, [700], [20], 4, 1, D, 9.0, small=0.02, grows=grows, growth=growth, kind="sparse")
+    for ctas in (1, 2):
+        c.check(*c.run(ctas=ctas))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("poison", [float("inf"), float("nan"), 1e30])
+def test_the_values_of_masked_nodes_do_not_matter(D, poison):
+    """A node that only itself sees, with scales of any value: the other rows as if it were
+    not there."""
+    c = Sink(44, [90], [24], 4, 1, D, 9.0, small=0.02)
+    c.masks &= np.uint32(~(1 << 13) & 0xffffffff)
+    c.masks[13] |= np.uint32(1 << 13)
+    want = c.run(ctas=1)
+    c.check(*want)
+    rest = [r for r in range(24) if r != 13]
+    pg, s = c.table[0, 103 // 16], 103 % 16
+    for t in c.dev[2:]:
+        t[pg, :, s] = poison
+    got = c.run(ctas=1)
+    for a, b in zip(want, got):
+        assert torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_same_call_again_and_the_same_bits(D):
+    c = Sink(45, [3000, 40], [30, 64], 8, 2, D, 9.0, small=0.02, grows=900, growth=50.0)
+    want = c.run()
+    for _ in range(20):
+        got = c.run()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
