@@ -543,6 +543,11 @@ __device__ __noinline__ float2 largest_seen(const float* vs, int quad, uint32_t 
   return make_float2(v[0], v[1]);
 }
 
+// The smallest of the warp's values, none below 0 (so they order as whole numbers).
+__device__ __forceinline__ float warp_lowest(float v) {
+  return __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(v)));
+}
+
 // ------------------------------------------------------------------- kernel
 // kSwa: sliding-window instantiation (window read from the parameters); the
 // plain one compiles the window bounds out. kItems: the plan holds prefix
@@ -802,7 +807,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         // base: rowfac * (running maximum) - log2 f; limit: the x that moves it; v_top: the V
         // scale that lowers f
         float limit[2] = {-INFINITY, -INFINITY};
-        float v_top[2] = {127.f, 127.f}, v_low = 127.f;
+        float v_top[2] = {127.f, 127.f}, v_low = INFINITY;
         for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
           const int st = g % kStages;
           // (the QK issuer has waited for the tile's scales)
@@ -899,7 +904,12 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
                   sum[k] = make_float2(sum[k].x * alpha[k], sum[k].y * alpha[k]);
                 }
               }
-              v_low = k1_live ? fminf(v_top[0], v_top[1]) : v_top[0];
+              // a lane looks at its two keys for all rows that have seen any
+              v_low = INFINITY;
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (rr[k] >= 0 && limit[k] > -INFINITY) v_low = fminf(v_low, v_top[k]);
+              v_low = warp_lowest(v_low);
             }
             float2 vs2[8];
 #pragma unroll

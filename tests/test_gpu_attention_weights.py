@@ -48,20 +48,23 @@ class Sink(Case):
         self.pool.k_scales, self.pool.v_scales = self.scales[0], self.scales[1]
         self.dev = (codes[:, :, 0], codes[:, :, 1], torch.tensor(self.scales[0], device="cuda"),
                     torch.tensor(self.scales[1], device="cuda"))
-        self.want = None
+        self.want, self.big = None, unit * max(1.0, growth) > 1e20
 
     def check(self, out, lse, rows=slice(None)):
         if self.want is None:
+            # (poisoned scales are read as what they are: rows that see them are not looked at)
             self.want = T.attention(self.q.double().cpu().numpy(), self.pool, self.table, self.ctx,
                                     self.lens, self.masks, self.hkv, self.sm)
         want, wl, (av, qk, total) = self.want
         o, got = out[:self.n].double().cpu().numpy(), lse[:self.n].double().cpu().numpy()
         keys = max(c + t for c, t in zip(self.ctx, self.lens))
-        M = max(self.scales[1, self.table[b, j // 16], :, j % 16].max()
-                for b in range(len(self.ctx)) for j in range(self.ctx[b] + self.lens[b]))
+        M = max(m for b in range(len(self.ctx)) for j in range(self.ctx[b] + self.lens[b])
+                for m in self.scales[1, self.table[b, j // 16], :, j % 16] if m < 1e29 or self.big)
         d = 2 * (self.D + 8) * 2.0 ** -24 * qk + 2.0 ** -21
         live = ~np.isneginf(wl)
-        assert np.array_equal(np.isneginf(got), ~live) and not o[~live].any()
+        live[[r for r in range(self.n) if r not in np.arange(self.n)[rows]]] = False
+        none = np.isneginf(wl)[rows]
+        assert np.array_equal(np.isneginf(got)[rows], none) and not o[rows][none].any()
         off = np.abs(got - wl)[live]
         assert (off <= (d + 2.0 ** -21)[live] + 2.0 ** -22 * np.abs(wl[live])).all(), off.max()
         bound = 2.0 ** -8 * np.abs(want) + (2 * d[..., None] + 2.0 ** -11) * av \
@@ -117,6 +120,27 @@ def test_the_values_of_masked_nodes_do_not_matter(D, poison):
     got = c.run(ctas=1)
     for a, b in zip(want, got):
         assert torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.parametrize("poison", [float("inf"), 1e30])
+def test_a_row_with_scales_of_its_own_does_not_hide_the_others(poison):
+    """One node that only itself sees with a scale of any value, in the first tile, then one
+    large value after another in the second."""
+    c = Sink(46, [32], [96], 1, 1, 64, 9.0, small=0.02, kind="full")
+    c.masks[:, 0] &= np.uint32(0xffffffff ^ (1 << 13))
+    c.masks[13] = 0
+    c.masks[13, 0] = 1 << 13
+    rest = [r for r in range(96) if r != 13]
+    c.scales[1, c.table[0, 45 // 16], :, 45 % 16] = poison
+    for j in range(64, 128):
+        at = (1, c.table[0, j // 16], slice(None), j % 16)
+        was = c.scales[at].copy()
+        c.scales[at] = 1e7
+        c.dev = (*c.dev[:3], torch.tensor(c.scales[1], device="cuda"))
+        c.want = None
+        with np.errstate(all="ignore"):
+            c.check(*c.run(ctas=1), rows=rest)
+        c.scales[at] = was
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
