@@ -7,13 +7,14 @@
 // rows (the reuse across query heads and verify tokens):
 //
 //   S  = Q' . C_K^T            tcgen05.mma kind::f16, A = Q' (TMEM), B = K tile (SMEM)
-//   s' = S * sK_j  ;  p = exp2(f_r * (s' - m_r))   (f_r = sm_scale*log2e / 2^e_r)
+//   s' = S * sK_j  ;  p = exp2(f_r * (s' - m_r)) * u_r   (f_r = sm_scale*log2e / 2^e_r)
 //   O += (p * sV_j) . C_V      tcgen05.mma kind::f16, A = P (TMEM), B = V tile (SMEM)
 //
 // Q' = Q * 2^e_r per row, e_r chosen so max|Q'| is in [2^14, 2^15): an exact
 // power-of-two rescale that lets bf16 Q enter the fp16 MMA exactly (int8 codes
 // are exact in fp16). The K scale multiplies score columns, the V scale is
-// folded into P before P is rounded to fp16.
+// folded into P before P is rounded to fp16; u_r is a power of two that keeps
+// small weights among fp16's normal numbers (v_top_for).
 //
 // Warp roles (512 threads):
 //   warps 0-7   softmax + epilogue: warp w owns TMEM lanes 32(w%4) + 16(w/4)
@@ -97,15 +98,16 @@ constexpr float kRescaleLog2 = 8.0f;          // lazy rescale threshold (factor 
 // The products p * s_V are rounded to fp16 on their way to the second MMA. V scales are
 // about 0.01, so that a weight below 2^-8 of the largest would already lose bits there and
 // one below 2^-18 be nothing: with a sink that holds most of the weight that is much of
-// the output. So a row's weights carry a power of two f that puts the largest V scale it
-// has seen at 2^5 <= f s_V < 2^7 (p * f * s_V < 2^15, which leaves the reference's rounding
-// a factor of two). It is chosen with the row's first key, lowered where a larger scale
-// comes, and cancels in O / l. A row holds 127 / f, the largest scale that f still serves.
-// (f stays within 2^-96 .. 2^64, so that sums of weights stay normal fp32 numbers: below
-// V scales of 2^-59 products get small again, above 2^103 they overflow.)
+// the output. So a row's weights carry a power of two u that puts the largest V scale it
+// has seen at 2^5 <= u s_V < 2^7 (p s_V < 2^15, which leaves the reference's rounding a
+// factor of two). It is chosen with the row's first key, lowered where a larger scale
+// comes, and cancels in O / l. A row holds 127 / u, the largest scale that u still serves.
+// (u stays within 2^-96 .. 2^30, so that it can fall from one end to the other and leave the
+// weights before it normal fp32 numbers: V scales below 2^-25 lose bits as all did, above
+// 2^103 the products overflow.)
 __device__ __forceinline__ float v_top_for(float scale) {
-  const int e = 132 - (int)(__float_as_uint(scale) >> 23);       // f = 2^e, f * scale in [32, 64)
-  return __uint_as_float((uint32_t)(133 - max(-96, min(64, e))) << 23 | 0x7e0000u);
+  const int e = 132 - (int)(__float_as_uint(scale) >> 23);       // u = 2^e, u * scale in [32, 64)
+  return __uint_as_float((uint32_t)(133 - max(-96, min(30, e))) << 23 | 0x7e0000u);
 }
 __device__ __forceinline__ int v_factor_log2(float v_top) {
   return 133 - (int)(__float_as_uint(v_top) >> 23);
@@ -524,8 +526,8 @@ __device__ __forceinline__ void convert_codes_fast(const uint8_t* src, uint8_t* 
 }
 
 // The largest of 16 keys' V scales among those that two rows see (bits m0 and m1), for a
-// tile with nodes: a masked key's scale may be anything, and is not to touch f. Called
-// where f is chosen or lowered only, and out of line: inlined it cost the whole loop
+// tile with nodes: a masked key's scale may be anything, and is not to touch u. Called
+// where u is chosen or lowered only, and out of line: inlined it cost the whole loop
 // registers (32 ragged sequences 155 -> 165 us, heads of 128 180 -> 191; like this 155
 // and 186).
 __device__ __noinline__ float2 largest_seen(const float* vs, int quad, uint32_t m0, uint32_t m1) {
@@ -542,6 +544,9 @@ __device__ __noinline__ float2 largest_seen(const float* vs, int quad, uint32_t 
   }
   return make_float2(v[0], v[1]);
 }
+
+// The low n of 16 bits (none below 0, all from 16 on).
+__device__ __forceinline__ uint32_t low_bits16(int n) { return (1u << max(0, min(16, n))) - 1; }
 
 // The smallest of the warp's values, none below 0 (so they order as whole numbers).
 __device__ __forceinline__ float warp_lowest(float v) {
@@ -708,8 +713,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         if constexpr (kItems || kTree) {
           const int j = s.r0 + (live[k] ? r : 0);
           const int tt = j / G, gg = j - tt * G;
-          // last visible key of the row (of a tree: the row of its mask)
-          lim[k] = kTree ? s.qbase + tt : s.ctx + tt;
+          lim[k] = s.ctx + tt;                            // last visible key (chains)
           lo[k] = 0;
           qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + gg;
         } else {
@@ -755,7 +759,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           rowfac[k] = p.sm_scale_log2 / up[k];
           // (trees: never 0, or a masked key's -inf would come out as NaN; such a row's
           // scores are 0 either way)
-          if constexpr (kTree) rowfac[k] = fmaxf(rowfac[k], 1.17549435e-38f);
+          rowfac[k] = fmaxf(rowfac[k], 1.17549435e-38f);
         }
         static_assert(D == 64 || (D / 2) % 64 == 0, "Q' stores of 64 packed columns, or 32");
         if constexpr (D == 64) {
@@ -793,217 +797,38 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       fence_before();
       warp_arrive(smem_u32(&sh->q_full), lane);
 
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // l: this thread's columns
-      float down[2] = {1.f, 1.f};                         // 1 / f
-      if constexpr (kTree) {
-        // A softmax warp takes its tiles one after the other, and with 2 of them a
-        // scheduler their latency bounds the kernel. So the chain of a tile is kept short:
-        // the running maximum is looked at by each thread for its own keys, and only where
-        // one passes it by more than 2^8 is it reduced over the row and moved, with O and
-        // the sums (the same decisions as a reduction every tile would take; 306 -> 285 us
-        // for 16 x 32768 keys).
-        float base[2] = {0.f, 0.f};
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // base: rowfac * (running maximum) - log2 f; limit: the x that moves it; v_top: the V
-        // scale that lowers f
-        float limit[2] = {-INFINITY, -INFINITY};
-        float v_top[2] = {127.f, 127.f}, v_low = INFINITY;
-        for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
-          const int st = g % kStages;
-          // (the QK issuer has waited for the tile's scales)
-          const float* ks = scales + sst * 2 * kTileKeys;
-          const float* vs = ks + kTileKeys;
-          ok = sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;                                   // a timeout seen by some lanes
-          fence_after();
-          if (warp_live) {
-            uint32_t pw[16];                                // P: 32 packed columns
-            uint32_t sv[32];
-            tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
-            const int k0 = it * kTileKeys;
-            float2 x[2][8], ks2[8];
-            // two of the tile's V scales in a lane, all 64 in the warp
-            const float2 vq2 = *reinterpret_cast<const float2*>(
-                vs + 16 * quad + 4 * ((lane >> 3) ^ quad) + 2 * (lane >> 2 & 1));
-            const float vt = fmaxf(fabsf(vq2.x), fabsf(vq2.y));
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-              const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
-              ks2[2 * i4] = make_float2(kq.x, kq.y);
-              ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
-            }
-            tmem_wait_ld(sv);         // sv is read only after the wait
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                x[k][i] = __fmul2_rn(make_float2(__uint_as_float(sv[4 * i + 2 * k]),
-                                                 __uint_as_float(sv[4 * i + 2 * k + 1])), ks2[i]);
-            // which of this thread's keys (16 * quad + 2i + {0,1}) the rows see
-            uint32_t vm[2] = {0xffffu, 0xffffu};
-            bool full = true;
-            if (k0 + kTileKeys > s.ctx) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                if (rr[k] >= 0) {
-                  const int row = s.qbase + (s.r0 + rr[k]) / G;
-                  vm[k] = tree_bits16(p.tree_masks + (size_t)row * p.mask_stride,
-                                      k0 + 16 * quad - s.ctx, s.T);
-                }
-                full = full && vm[k] == 0xffffu;
-              }
-              if (!full) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    if (!(vm[k] >> (2 * i) & 1)) x[k][i].x = -INFINITY;
-                    if (!(vm[k] >> (2 * i + 1) & 1)) x[k][i].y = -INFINITY;
-                  }
-              }
-            }
-            float mt[2], alpha[2] = {1.f, 1.f};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              mt[k] = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) mt[k] = fmax3(mt[k], x[k][i].x, x[k][i].y);
-            }
-            if (__any_sync(0xffffffffu, vt > v_low || mt[0] > limit[0] ||
-                                            (k1_live && mt[1] > limit[1]))) {
-              // the largest V scale that a row sees: of a tile with nodes the row's own
-              float v[2];
-              v[0] = v[1] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vt)));
-              if (k0 + kTileKeys > s.ctx) {
-                const float2 own = largest_seen(vs, quad, vm[0], vm[1]);
-                v[0] = own.x;
-                v[1] = own.y;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 1));
-                  v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 2));
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float t = mt[k];
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                const bool first = limit[k] == -INFINITY, moves = t > limit[k];
-                if (first ? moves : moves || v[k] > v_top[k]) {  // the same in the row's threads
-                  float ref = base[k] + (float)v_factor_log2(v_top[k]);
-                  if (moves) {
-                    ref = rowfac[k] * t;
-                    limit[k] = t + kRescaleLog2 / rowfac[k];
-                  }
-                  if (first || v[k] > v_top[k]) v_top[k] = v_top_for(v[k]);
-                  ref -= (float)v_factor_log2(v_top[k]);
-                  alpha[k] = first ? 0.f : ex2(base[k] - ref);
-                  base[k] = ref;
-                  sum[k] = make_float2(sum[k].x * alpha[k], sum[k].y * alpha[k]);
-                }
-              }
-              // a lane looks at its two keys for all rows that have seen any
-              v_low = INFINITY;
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                if (rr[k] >= 0 && limit[k] > -INFINITY) v_low = fminf(v_low, v_top[k]);
-              v_low = warp_lowest(v_low);
-            }
-            float2 vs2[8];
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-              const float4 vq4 = *reinterpret_cast<const float4*>(vs + 16 * quad + 4 * (i4 ^ quad));
-              vs2[2 * i4] = make_float2(vq4.x, vq4.y);
-              vs2[2 * i4 + 1] = make_float2(vq4.z, vq4.w);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if (k == 1 && !k1_live) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) pw[2 * i + 1] = 0u;
-                break;
-              }
-              const float2 rf2 = make_float2(rowfac[k], rowfac[k]);
-              const float2 nb2 = make_float2(-base[k], -base[k]);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float2 vq = vs2[i];
-                if (!full) {      // scales of masked keys are not trusted
-                  if (!(vm[k] >> (2 * i) & 1)) vq.x = 0.f;
-                  if (!(vm[k] >> (2 * i + 1) & 1)) vq.y = 0.f;
-                }
-                const float2 e0 = __ffma2_rn(x[k][i], rf2, nb2);
-                const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
-                sum[k] = __fadd2_rn(sum[k], p0);
-                __half2 h0 = __float22half2_rn(__fmul2_rn(p0, vq));
-                pw[2 * i + k] = *reinterpret_cast<uint32_t*>(&h0);   // packed column 4i + quad
-              }
-            }
-            // O follows once the previous tile's PV is done (the first tile's PV does
-            // not add to O). p_free of that tile's buffer: its previous phase (PV three
-            // tiles back) is complete, so a parity wait cannot be satisfied by an older one.
-            if (it > s.i0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-              ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->p_free[(g - 1) % kStages]),
-                                                     ((g - 1) / kStages) & 1));
-              if (!ok) break;
-              fence_after();
-#pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 64) {
-                uint32_t v[32];
-                tmem_ld16x256_x8(tmem + lane_base + C::kOCol + c0, v);
-                tmem_wait_ld(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    v[4 * i + 2 * k] = __float_as_uint(__uint_as_float(v[4 * i + 2 * k]) * alpha[k]);
-                    v[4 * i + 2 * k + 1] =
-                        __float_as_uint(__uint_as_float(v[4 * i + 2 * k + 1]) * alpha[k]);
-                  }
-                tmem_st16x256_x8(tmem + lane_base + C::kOCol + c0, v);
-              }
-            }
-            tmem_st16x128_x8(tmem + lane_base + C::kSCol + st * kTileKeys, pw);
-            tmem_wait_st();
-          }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&sh->p_full[st]));
-            mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
-          }
-          if (++sst == kScStages) sst = 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          m[k] = base[k] + (float)v_factor_log2(v_top[k]);   // rowfac * m
-          down[k] = __uint_as_float((uint32_t)(127 - v_factor_log2(v_top[k])) << 23);
-          l[k] = sum[k].x + sum[k].y;
-          // the row again, from what was kept of it
-          live[k] = rr[k] >= 0;
-          const int j = s.r0 + max(rr[k], 0), tt = j / G;
-          qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + (j - tt * G);
-        }
-      } else {
+      // A softmax warp takes its tiles one after the other, and with 2 of them a
+      // scheduler their latency bounds the kernel. So the chain of a tile is kept short:
+      // the running maximum is looked at by each thread for its own keys, and only where
+      // one passes it by more than 2^8 is it reduced over the row and moved, with O and
+      // the sums (the same decisions as a reduction every tile would take; trees 306 -> 285
+      // us for 16 x 32768 keys, chains of 4 tokens 269 -> 261, with u counted in).
+      float base[2] = {0.f, 0.f};
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // base: rowfac * (running maximum) - log2 u; limit: the x that moves it; v_top: the V
+      // scale that lowers u
+      float limit[2] = {-INFINITY, -INFINITY};
+      float v_top[2] = {127.f, 127.f}, v_low = INFINITY;
       for (int it = s.i0; it < s.i1 && ok; ++it, ++g) {
-        const int st = g % kStages, sst = g % kScStages;
-        ok = sync.wait(smem_u32(&sh->sc_full[sst]), (g / kScStages) & 1) &&
+        const int st = g % kStages;
+        const float* ks = scales + sst * 2 * kTileKeys;
+        const float* vs = ks + kTileKeys;
+        // (trees: the QK issuer has waited for the tile's scales)
+        ok = (kTree || sync.wait(smem_u32(&sh->sc_full[sst]), (g / kScStages) & 1)) &&
              sync.wait(smem_u32(&sh->s_full[st]), (g / kStages) & 1);
-        ok = __all_sync(0xffffffffu, ok);       // a timeout seen by some lanes stops the warp
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;                                   // a timeout seen by some lanes
         fence_after();
-        uint32_t pw[16];                                   // P: 32 packed columns
-        float alpha[2] = {1.f, 1.f};
         if (warp_live) {
-          const int k0 = it * kTileKeys;
-          const float* ks = scales + sst * 2 * kTileKeys;
-          const float* vs = ks + kTileKeys;
+          uint32_t pw[16];                                // P: 32 packed columns
           uint32_t sv[32];
           tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
-          // the K scales load while the TMEM load is in flight
-          float2 ks2[8], x[2][8];
+          const int k0 = it * kTileKeys;
+          float2 x[2][8], ks2[8];
+          // two of the tile's V scales in a lane, all 64 in the warp
+          const float2 vq2 = *reinterpret_cast<const float2*>(
+              vs + 16 * quad + 4 * ((lane >> 3) ^ quad) + 2 * (lane >> 2 & 1));
+          const float vt = fmaxf(fabsf(vq2.x), fabsf(vq2.y));
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
@@ -1011,73 +836,88 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             ks2[2 * i4 + 1] = make_float2(kq.z, kq.w);
           }
           tmem_wait_ld(sv);         // sv is read only after the wait
-          // x = S * sK (packed fp32x2); masked columns -> -inf (their scales
-          // are not read: pages past the end may hold anything)
-          // this thread's keys: 16*quad + 2i + {0,1} (see tile_row_of_key)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              x[k][i] = (k == 0 || k1_live)
-                            ? __fmul2_rn(make_float2(__uint_as_float(sv[4 * i + 2 * k]),
-                                                     __uint_as_float(sv[4 * i + 2 * k + 1])), ks2[i])
-                            : make_float2(-INFINITY, -INFINITY);
-          }
-          // tile keys jj with nlo <= jj < nvis are visible to the row
-          int nvis[2] = {kTileKeys, kTileKeys}, nlo[2] = {-1, -1};
+              x[k][i] = __fmul2_rn(make_float2(__uint_as_float(sv[4 * i + 2 * k]),
+                                               __uint_as_float(sv[4 * i + 2 * k + 1])), ks2[i]);
+          // which of this thread's keys (16 * quad + 2i + {0,1}) the rows see
+          uint32_t vm[2] = {0xffffu, 0xffffu};
           bool full = true;
-          // a tile below the block's keys (and, with a window, above every
-          // row's lower bound) is visible to every row: no per-row bounds
-          const bool tile_inside = k0 + kTileKeys <= s.ctx &&
-                                   (!kSwa || s.ctx + s.T - window <= k0);
-          if (!tile_inside) {
+          const bool edge = k0 + kTileKeys > s.ctx || (kSwa && s.ctx + s.T - window > k0);
+          if (edge) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              nvis[k] = live[k] ? min(kTileKeys, lim[k] - k0 + 1) : 0;
-              nlo[k] = kSwa ? max(lo[k] - k0, -1) : -1;       // compile-time -1 without a window
-              // rows that hold no query row need no mask (their P only reaches
-              // output rows that are never read)
-              full = full && (!live[k] || (nvis[k] == kTileKeys && (!kSwa || nlo[k] <= 0)));
+              if (rr[k] >= 0) {
+                if constexpr (kTree) {
+                  const int row = s.qbase + (s.r0 + rr[k]) / G;
+                  vm[k] = tree_bits16(p.tree_masks + (size_t)row * p.mask_stride,
+                                      k0 + 16 * quad - s.ctx, s.T);
+                } else {
+                  const int j0 = k0 + 16 * quad;
+                  vm[k] = low_bits16(lim[k] - j0 + 1) & (kSwa ? ~low_bits16(lo[k] - j0) : ~0u);
+                }
+              }
+              full = full && vm[k] == 0xffffu;
+            }
+            if (!full) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (!(vm[k] >> (2 * i) & 1)) x[k][i].x = -INFINITY;
+                  if (!(vm[k] >> (2 * i + 1) & 1)) x[k][i].y = -INFINITY;
+                }
             }
           }
-          if (!full) {
+          float mt[2], alpha[2] = {1.f, 1.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mt[k] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mt[k] = fmax3(mt[k], x[k][i].x, x[k][i].y);
+          }
+          if (__any_sync(0xffffffffu, vt > v_low || mt[0] > limit[0] ||
+                                          (k1_live && mt[1] > limit[1]))) {
+            // the largest V scale that a row sees: of a tile with nodes the row's own
+            float v[2];
+            v[0] = v[1] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vt)));
+            if (edge) {
+              const float2 own = largest_seen(vs, quad, vm[0], vm[1]);
+              v[0] = own.x;
+              v[1] = own.y;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 1));
+                v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], 2));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float t = mt[k];
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+              const bool first = limit[k] == -INFINITY, moves = t > limit[k];
+              if (first ? moves : moves || v[k] > v_top[k]) {  // the same in the row's threads
+                float ref = base[k] + (float)v_factor_log2(v_top[k]);
+                if (moves) {
+                  ref = rowfac[k] * t;
+                  limit[k] = t + __fdividef(kRescaleLog2, rowfac[k]);   // (a bound, no result)
+                }
+                if (first || v[k] > v_top[k]) v_top[k] = v_top_for(v[k]);
+                ref -= (float)v_factor_log2(v_top[k]);
+                alpha[k] = first ? 0.f : ex2(base[k] - ref);
+                base[k] = ref;
+                sum[k] = make_float2(sum[k].x * alpha[k], sum[k].y * alpha[k]);
+              }
+            }
+            // a lane looks at its two keys for all rows that have seen any
+            v_low = INFINITY;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int j = 16 * quad + 2 * i;
-                if (j >= nvis[k] || j < nlo[k]) x[k][i].x = -INFINITY;
-                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) x[k][i].y = -INFINITY;
-              }
-          }
-          float base[2] = {0.f, 0.f};
-          // both row sets' maxima at once (independent chains); the second is
-          // unused when the warp's second row set holds no row
-          float mts[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mts[k] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mts[k] = fmax3(mts[k], x[k][i].x, x[k][i].y);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) mts[k] = fmaxf(mts[k], __shfl_xor_sync(0xffffffffu, mts[k], 1));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) mts[k] = fmaxf(mts[k], __shfl_xor_sync(0xffffffffu, mts[k], 2));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k == 1 && !k1_live) break;                // no row in the warp's second set
-            const float mt = mts[k];
-            const float m_new = fmaxf(m[k], mt);
-            float m_use = m[k];
-            if (m[k] == -INFINITY) {
-              m_use = m_new;
-            } else if (rowfac[k] * (m_new - m[k]) > kRescaleLog2) {
-              alpha[k] = ex2(rowfac[k] * (m[k] - m_new));
-              m_use = m_new;
-            }
-            m[k] = m_use;
-            base[k] = (m_use == -INFINITY) ? 0.f : rowfac[k] * m_use;
+              if (rr[k] >= 0 && limit[k] > -INFINITY) v_low = fminf(v_low, v_top[k]);
+            v_low = warp_lowest(v_low);
           }
           float2 vs2[8];
 #pragma unroll
@@ -1095,58 +935,66 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             }
             const float2 rf2 = make_float2(rowfac[k], rowfac[k]);
             const float2 nb2 = make_float2(-base[k], -base[k]);
-            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float2 vq = vs2[i];
               if (!full) {      // scales of masked keys are not trusted
-                const int j = 16 * quad + 2 * i;
-                if (j >= nvis[k] || j < nlo[k]) vq.x = 0.f;
-                if (j + 1 >= nvis[k] || j + 1 < nlo[k]) vq.y = 0.f;
+                if (!(vm[k] >> (2 * i) & 1)) vq.x = 0.f;
+                if (!(vm[k] >> (2 * i + 1) & 1)) vq.y = 0.f;
               }
               const float2 e0 = __ffma2_rn(x[k][i], rf2, nb2);
               const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
-              acc = __fadd2_rn(acc, p0);
+              sum[k] = __fadd2_rn(sum[k], p0);
               __half2 h0 = __float22half2_rn(__fmul2_rn(p0, vq));
               pw[2 * i + k] = *reinterpret_cast<uint32_t*>(&h0);   // packed column 4i + quad
             }
-            l[k] = l[k] * alpha[k] + (acc.x + acc.y);
           }
-        }
-        // a rescale of O waits for the previous tile's PV (rare: the running
-        // max is only moved when it grows by more than 2^8). p_free of that
-        // tile's buffer: its previous phase (PV three tiles back) is complete,
-        // so a parity wait cannot be satisfied by an older phase.
-        if (it > s.i0 && warp_live &&
-            __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-          ok = __all_sync(0xffffffffu,
-                          sync.wait(smem_u32(&sh->p_free[(g - 1) % kStages]), ((g - 1) / kStages) & 1));
-          if (!ok) break;
-          fence_after();
+          // O follows once the previous tile's PV is done (the first tile's PV does
+          // not add to O). p_free of that tile's buffer: its previous phase (PV kStages + 1
+          // tiles back) is complete, so a parity wait cannot be satisfied by an older one.
+          if (it > s.i0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->p_free[(g - 1) % kStages]),
+                                                   ((g - 1) / kStages) & 1));
+            if (!ok) break;
+            fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 64) {
-            uint32_t v[32];
-            tmem_ld16x256_x8(tmem + lane_base + C::kOCol + c0, v);
-            tmem_wait_ld(v);
+            for (int c0 = 0; c0 < D; c0 += 64) {
+              uint32_t v[32];
+              tmem_ld16x256_x8(tmem + lane_base + C::kOCol + c0, v);
+              tmem_wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                v[4 * i + 2 * k] = __float_as_uint(__uint_as_float(v[4 * i + 2 * k]) * alpha[k]);
-                v[4 * i + 2 * k + 1] =
-                    __float_as_uint(__uint_as_float(v[4 * i + 2 * k + 1]) * alpha[k]);
-              }
-            tmem_st16x256_x8(tmem + lane_base + C::kOCol + c0, v);
+                for (int k = 0; k < 2; ++k) {
+                  v[4 * i + 2 * k] = __float_as_uint(__uint_as_float(v[4 * i + 2 * k]) * alpha[k]);
+                  v[4 * i + 2 * k + 1] =
+                      __float_as_uint(__uint_as_float(v[4 * i + 2 * k + 1]) * alpha[k]);
+                }
+              tmem_st16x256_x8(tmem + lane_base + C::kOCol + c0, v);
+            }
           }
-        }
-        warp_arrive(smem_u32(&sh->sc_free[sst]), lane);    // scales of this tile are read
-        if (warp_live) {
           tmem_st16x128_x8(tmem + lane_base + C::kSCol + st * kTileKeys, pw);
           tmem_wait_st();
         }
         fence_before();
-        warp_arrive(smem_u32(&sh->p_full[st]), lane);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh->p_full[st]));
+          mbar_arrive(smem_u32(&sh->sc_free[sst]));        // the scales are read
+        }
+        if (++sst == kScStages) sst = 0;
       }
+      float m[2], l[2], down[2];                          // l: this thread's columns; down: 1 / u
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[k] = base[k] + (float)v_factor_log2(v_top[k]);   // rowfac * m
+        down[k] = __uint_as_float((uint32_t)(127 - v_factor_log2(v_top[k])) << 23);
+        l[k] = sum[k].x + sum[k].y;
+        if constexpr (kTree) {                          // the row again, from what was kept of it
+          live[k] = rr[k] >= 0;
+          const int j = s.r0 + max(rr[k], 0), tt = j / G;
+          qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + (j - tt * G);
+        }
       }
       if (!ok) break;
       // epilogue: last PV of the segment complete -> normalise, write out
@@ -1200,7 +1048,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           if (live[k] && quad == 0) {
             const float lse =
                 l[k] > 0.f
-                    ? ((kTree ? m[k] : rowfac[k] * m[k]) + __log2f(l[k] * down[k])) *
+                    ? (m[k] + __log2f(l[k] * down[k])) *
                           0.69314718055994531f
                     : -INFINITY;
             if (ns == 1) p.lse[qrow_off[k]] = lse;
