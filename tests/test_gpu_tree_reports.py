@@ -1,4 +1,5 @@
-"""What the tree operators report: unusable offsets whatever else the call holds."""
+"""What the tree operators report: unusable offsets whatever else the call holds, and waits
+that run out."""
 from __future__ import annotations
 
 import pytest
@@ -11,7 +12,7 @@ if not torch.cuda.is_available():
 
 from speculative_verify_attention_kv_gb300 import splash_kv as sk  # noqa: E402
 
-from test_gpu_tree_attention import i32  # noqa: E402
+from test_gpu_tree_attention import Case, i32  # noqa: E402
 
 
 @pytest.mark.parametrize("offsets", [[0, 9, 4], [0, 3, 2], [-1, 2, 6], [0, 2, 7]])
@@ -42,3 +43,27 @@ def test_what_accept_writes_for_unusable_offsets_is_reported_by_compact_too():
     sk.splash_kv_compact(*sk.alloc_pool(2, 1, 64), i32([1, 2, 3]), rows, offsets, acc,
                          device_status=status)
     assert status.item() == sk.DEVICE_BAD_LENGTH
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_runs_out_within_a_few_calls(D):
+    """One CTA, 20000 keys and a limit of 1 ns: hundreds of waits for copies and for other
+    roles. The hardware may let each sleep past the clock's first look, all of them in six
+    calls no. Each such call reports it, and the next with the usual limit is as before."""
+    c = Case(23, [20000, 64, 5], [40, 3, 17], 8, 2, D)
+    want, status, ran_out = c.run(ctas=1), i32([0]), 0
+    for _ in range(6):
+        status.zero_()
+        prev = sk.splash_set_wait_limit_ns(1)
+        try:
+            c.run(status=status, ctas=1)
+            torch.cuda.synchronize()
+        finally:
+            sk.splash_set_wait_limit_ns(prev)
+        assert status.item() in (0, sk.DEVICE_TIMEOUT)
+        ran_out += status.item() == sk.DEVICE_TIMEOUT
+        status.zero_()
+        got = c.run(status=status, ctas=1)
+        assert status.item() == 0
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert ran_out
