@@ -77,9 +77,9 @@ __device__ inline float warp_fmax(float v) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
   return y;
 }
-// x as a whole number of the same order; -0 as 0, NaN as -inf.
+// x as a whole number of the same order; -0 as 0, NaN as -inf, infinity as the largest finite.
 __device__ inline uint32_t ordered(float x) {
-  if (!(x >= -INFINITY)) x = -INFINITY;
+  x = x >= -INFINITY ? fminf(x, kMaxFinite) : -INFINITY;
   const uint32_t u = __float_as_uint(x + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_jo
     }
     s.key[tid] = (unsigned long long)ordered(mine) << 32 | (uint32_t)~tid;
     __syncthreads();
-    if (rank_of(s.key, kThreads, s.key[tid]) == p.top - 1) s.least = mine;
+    if (rank_of(s.key, kThreads, s.key[tid]) == p.top - 1) s.least = fminf(mine, kMaxFinite);
     __syncthreads();
   }
   // vectors with a value that reaches the last of those maxima: a warp per segment,

@@ -134,3 +134,20 @@ def test_large_values_of_both_signs(kind):
     o, st = run(z, tokens, K)
     assert st == 0
     near(z, tokens, o)
+
+
+@pytest.mark.parametrize("V", [24, 600, 40000])
+@pytest.mark.parametrize("k", [2, 5, 32])
+def test_infinity_and_the_largest_finite_value_are_equal(V, k):
+    """The lowest index first, wherever the two stand; every one of them has ln p = -ln 4."""
+    z = torch.randn((2, V), generator=torch.Generator(device="cuda").manual_seed(V), device="cuda")
+    big, inf = torch.finfo(torch.float32).max, math.inf
+    z[0, 3], z[0, 10], z[0, 17], z[0, V - 1] = big, inf, big, inf
+    z[1, 3], z[1, 10], z[1, 17], z[1, V - 1] = inf, big, inf, big
+    o, st = run(z, [17, 17], k)
+    assert st == 0
+    for r in range(2):
+        assert o["top_ids"][r].tolist()[:4] == [3, 10, 17, V - 1][:k]
+    near4 = lambda x: (x.double() + math.log(4)).abs().max().item() <= 2.0 ** -18  # noqa: E731
+    assert near4(o["logprobs"]) and near4(o["top_logprobs"][:, :4])
+    assert near4(-o["entropy"])
