@@ -99,7 +99,6 @@ struct Vec<float> {
   static __device__ uint4 empty() {
     return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
   }
-  static __device__ void put(uint4& v, int i, float x) { (&v.x)[i] = __float_as_uint(x); }
   static __device__ float largest1(const uint4& v) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
                  fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
@@ -575,9 +574,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) logprobs_jo
     __syncthreads();
   }
   // vectors with a value that reaches the last of those maxima: a warp per segment,
-  // kBatch vectors on their way
+  // kBatch vectors of a lane on their way: those of five segments of 256 values, which is a
+  // warp's share (top / 4) up to top = 20; above, and with longer segments, another round
   const float least = s.least;
-  constexpr int kBatch = sizeof(T) == 4 ? 10 : 5;            // for 20 segments
+  constexpr int kBatch = 5 * kUnit / (32 * kPer);
   const int per_seg = seg_vecs / 32, steps = (p.top + kWarps - 1 - warp) / kWarps * per_seg;
   for (int s0 = 0; s0 < steps; s0 += kBatch) {
     uint4 x[kBatch];

@@ -58,8 +58,9 @@
 // For a tree of drafts (kTree) a unit is (sequence, KV head, row block): trees
 // with more than 128 rows take several. Its rows see the sequence's context and,
 // in the last tiles, the nodes whose bits their masks have: a thread takes the 16
-// bits of its keys from the mask words, once per row and tile, and nothing else
-// of the softmax differs. Only the tiles that hold nodes (5 at most) pay for it.
+// bits of its keys from the mask words, once per row and tile (a chain's come from
+// the row's bounds), and the rest of a tile's arithmetic is the same. Only the tiles
+// that hold nodes (5 at most) pay for it.
 // The cut of the stream over the CTAs is computed here, by every CTA for itself.
 // The roles differ in places, for a shorter chain and a ring that is free sooner: two
 // converter warps for K and two for V, one warp for all QK issues, warp 13 for the
@@ -84,7 +85,7 @@ constexpr int kPagesPerTile = kTileKeys / kPageSize;
 constexpr int kSoftmaxWarps = 8;              // 2 per TMEM lane quarter, 16 rows each
 constexpr int kLoadWarps = 4;
 constexpr int kLoadThreads = 32 * kLoadWarps;
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;   // TMEM allocation, QK issue (even tiles)
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;   // TMEM, QK issue (even tiles; trees: all)
 constexpr int kQkOddWarp = kMmaWarp + 1;                // QK issue (odd tiles)
 constexpr int kScaleWarp = kQkOddWarp;                  // trees: scales and prefetch instead
 constexpr int kPvWarp = kQkOddWarp + 1;                 // PV issue
@@ -127,7 +128,7 @@ struct Cfg {
   static_assert(kStages % 2 == 0, "QK-issuing warps by parity");
   static constexpr int kTileBytes = kTileKeys * D * 2;          // fp16 tile
   static constexpr int kQCol = 0;                                // Q': D/2 columns
-  static constexpr int kSCol = D / 2;                            // S[2]: 64 columns each
+  static constexpr int kSCol = D / 2;                            // S[kStages]: 64 columns each
   static constexpr int kOCol = D / 2 + kStages * kTileKeys;      // O: D columns
   static_assert(kOCol + D <= (int)kTmemCols, "TMEM budget");
   // staging ring stage: 4 (page, KV head) blocks of [K codes 16 x D][V codes 16 x D]
@@ -283,18 +284,18 @@ struct Smem {
                        kVStages = C::kVStages;
   uint64_t ring_full[kRing];      // producer tx (K and V codes) -> converters
   uint64_t ring_empty[2][kRing];  // converters done with a stage's [0] K / [1] V codes -> producer
-  uint64_t sc_full[kScStages];    // producer cp.async (scales) -> softmax
-  uint64_t sc_free[kScStages];    // softmax done with the scales -> producer
+  uint64_t sc_full[kScStages];    // cp.async of the scales -> softmax (trees: QK issuer)
+  uint64_t sc_free[kScStages];    // softmax done with the scales -> producer (trees: scale warp)
   uint64_t k_full[kStages];       // converters -> QK issuer (fp16 K of the tile ready)
   uint64_t v_full[kVStages];      // converters -> PV issuer (fp16 V of the tile ready)
   uint64_t k_free[kStages];       // QK done -> converters
-  uint64_t v_free[kVStages];      // PV done -> converters, producer (scales)
-  uint64_t s_full[kStages];       // QK done -> softmax
+  uint64_t v_free[kVStages];      // PV done -> converters
+  uint64_t s_full[kStages];       // QK done (trees: and the scales there) -> softmax
   uint64_t p_full[kStages];       // softmax -> MMA
   uint64_t p_free[kStages];       // PV of the buffer's tile done -> MMA (QK may
                                   // overwrite the S/P buffer), softmax (O rescale, epilogue)
   uint64_t q_full;                // softmax (Q' in TMEM) -> QK issuers
-  uint64_t q_ack;                 // both QK issuers saw q_full -> softmax (the next
+  uint64_t q_ack;                 // the QK issuers (chains: two) saw q_full -> softmax (the next
                                   // segment's Q' may complete q_full's next phase)
   uint64_t drain[3];              // QK even / QK odd / PV issuer: its MMAs complete
   uint32_t tmem_base;
@@ -446,11 +447,10 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
   constexpr int kQuartersPerPair = kChunks / 4;       // quarter warps per two key rows
   constexpr int kKeysPerPass = kLoadThreads * 16 / D;
   constexpr int kPer = kTileKeys / kKeysPerPass;
-  static_assert(kChunks % 4 == 0 && kTileKeys % kKeysPerPass == 0, "converter units");
+  static_assert(kChunks % 8 == 0 && kTileKeys % kKeysPerPass == 0, "converter units");
   const int w = lt >> 5, l = lt & 31, qtr = l >> 3, rsel = (l >> 2) & 1, j = l & 3;
   const int pair = qtr / kQuartersPerPair, qq = qtr % kQuartersPerPair;
-  // (a row of 64 codes is 4 chunks: a quarter warp takes both rows whole)
-  const int c16 = D == 64 ? j : 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
+  const int c16 = 8 * (qq >> 1) + 4 * (rsel ^ (qq & 1)) + j;
   const int key_in_pass = w * (32 * 16 / D) + 2 * pair + rsel;
   uint4 wv[kPer];
 #pragma unroll
@@ -474,7 +474,8 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst, 
   }
 }
 
-// The same by kWarps warps, with every address but the first a constant away: pass q's
+// The same by kWarps warps (trees; a row of 64 codes is 4 chunks, so that there a quarter
+// warp takes both rows whole), with every address but the first a constant away: pass q's
 // key and tile row differ from pass 0's by constants, and the swizzle's row bits are free
 // of carries, so that a store's address is one exclusive or (and an offset in the
 // instruction).
@@ -585,7 +586,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
   uint8_t* kbuf = smem + C::kOffK;
   uint8_t* vbuf = smem + C::kOffV;
   uint8_t* ring = smem + C::kOffRing;
-  float* scales = reinterpret_cast<float*>(smem + C::kOffScales);   // [3][K 64, V 64]
+  float* scales = reinterpret_cast<float*>(smem + C::kOffScales);   // [kScStages][K 64, V 64]
   Smem* sh = reinterpret_cast<Smem*>(smem + C::kOffBars);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -685,7 +686,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
     bool ok = true;
     uint32_t sst = 0;                                     // trees: tile g % kScStages
     while (ok && iter.next(s)) {
-      // Q' of this segment overwrites the previous one: both QK issuers must
+      // Q' of this segment overwrites the previous one: the QK issuers must
       // have seen the previous q_full phase (so neither lags it by two phases)
       if (nsegs > 0) {
         ok = __all_sync(0xffffffffu, sync.wait(smem_u32(&sh->q_ack), (nsegs - 1) & 1));
@@ -697,7 +698,7 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
       // q * rpq + i sits in lane 32q + i, i < rpq = ceil(R / 4). Lanes past
       // rpq in a quarter hold no row.
       const int rpq = (s.R + 3) >> 2;
-      int rr[2];                                          // row of each of this thread's lanes, -1: none
+      int rr[2];                                          // row of each of this thread's lanes, or -1
       bool live[2];
       int lim[2], lo[2];
       size_t qrow_off[2];
@@ -713,8 +714,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
         if constexpr (kItems || kTree) {
           const int j = s.r0 + (live[k] ? r : 0);
           const int tt = j / G, gg = j - tt * G;
-          lim[k] = s.ctx + tt;                            // last visible key (chains)
-          lo[k] = 0;
+          if constexpr (!kTree) {                         // (a tree's row has a mask)
+            lim[k] = s.ctx + tt;
+            lo[k] = 0;
+          }
           qrow_off[k] = (size_t)(s.qbase + tt) * p.num_q_heads + s.h * G + gg;
         } else {
           const int tt = live[k] ? r / G : 0, gg = live[k] ? r - tt * G : 0;
