@@ -828,10 +828,6 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
           tmem_ld16x256_x8(tmem + lane_base + C::kSCol + st * kTileKeys, sv);
           const int k0 = it * kTileKeys;
           float2 x[2][8], ks2[8];
-          // two of the tile's V scales in a lane, all 64 in the warp
-          const float2 vq2 = *reinterpret_cast<const float2*>(
-              vs + 16 * quad + 4 * ((lane >> 3) ^ quad) + 2 * (lane >> 2 & 1));
-          const float vt = fmaxf(fabsf(vq2.x), fabsf(vq2.y));
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             const float4 kq = *reinterpret_cast<const float4*>(ks + 16 * quad + 4 * (i4 ^ quad));
@@ -845,6 +841,10 @@ verify_tc_kernel(typename std::conditional<kTree, TreeAttnParams, AttnParams>::t
             for (int k = 0; k < 2; ++k)
               x[k][i] = __fmul2_rn(make_float2(__uint_as_float(sv[4 * i + 2 * k]),
                                                __uint_as_float(sv[4 * i + 2 * k + 1])), ks2[i]);
+          // two of the tile's V scales in a lane, all 64 in the warp
+          const float2 vq2 = *reinterpret_cast<const float2*>(
+              vs + 16 * quad + 4 * ((lane >> 3) ^ quad) + 2 * (lane >> 2 & 1));
+          const float vt = fmaxf(fabsf(vq2.x), fabsf(vq2.y));
           // which of this thread's keys (16 * quad + 2i + {0,1}) the rows see
           uint32_t vm[2] = {0xffffu, 0xffffu};
           bool full = true;
