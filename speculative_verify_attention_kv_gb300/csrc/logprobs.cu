@@ -6,7 +6,7 @@
 //
 // Reading the logits is the floor (HBM): 1500 rows of 131072 bf16 values 58 us, of which
 // the pass takes 64 and a call 74; 112 rows of 100003 fp32 values 6.6, 9.4 and 20. A value
-// costs the pass 8.7 instructions, which fill 72% of the issue slots: so the maximum is
+// costs the pass 9.0 instructions, which fill 73% of the issue slots: so the maximum is
 // taken on the values as stored, the sums run on pairs, and the reference m is moved only
 // where a block's maximum exceeds it by more than 2^8 (in e^: by 8 ln 2), for the whole
 // warp at once. A block is 1024 values, or 512 of fp32: four 16-byte loads a lane.

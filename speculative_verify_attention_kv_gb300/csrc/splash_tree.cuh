@@ -92,7 +92,8 @@ struct TreeLayout {
 // Batches that the attention kernel plans by itself, every CTA alike, with a thread
 // per sequence. It costs about what a launch before it would (5500 clocks, 3 us, at 16
 // sequences), but the pipeline's set-up and the tensor maps' fetch run beside it: a call
-// of one sequence 16.5 us, with the planner as a launch 18.5.
+// of one sequence 16.5 us, with the planner as a launch 18.5 (17.7 since weights carry a
+// factor for the V scales).
 constexpr int kTreeSelfPlan = 512;
 
 __host__ __device__ inline TreeLayout make_tree_layout(int B, int D, long long rows_bound) {

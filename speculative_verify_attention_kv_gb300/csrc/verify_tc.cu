@@ -67,8 +67,8 @@
 // scales and the prefetch, MMA issuers that run as whole warps with one lane issuing,
 // an S barrier that stands for the tile's scales too, and with heads of 64 or 128 four
 // S/P buffers and a ring of 8 or 5 stages. 16 sequences of 32768 keys, 16 nodes, 24
-// query and 4 KV heads: heads of 256 246 us a call (1.12 GB read, 4.7 TB/s in the
-// kernel), of 128 180 us, of 64 175 us. A tile takes 1.0, 0.75 and 0.7 us: a latency,
+// query and 4 KV heads: heads of 256 250 us a call (1.12 GB read, 4.6 TB/s in the
+// kernel), of 128 187 us, of 64 172 us. A tile takes 1.0, 0.75 and 0.7 us: a latency,
 // the softmax warps' way from S to P with the waits on both sides.
 #include <type_traits>
 
